@@ -10,6 +10,11 @@ The compute lives in ``libvqlinear.so`` (CUDA kernels behind the C ABI declared 
 
 from ._binding import (  # noqa: F401
     EXPORTS,
+    VQ_ACT_GELU,
+    VQ_ACT_GELU_TANH,
+    VQ_ACT_NONE,
+    VQ_ACT_RELU,
+    VQ_ACT_SILU,
     VQ_BF16,
     VQ_F16,
     VQ_FMT_RVQ12,
@@ -25,6 +30,7 @@ from ._binding import (  # noqa: F401
     VQError,
     load,
     make_codebooks,
+    make_epilogue,
     make_planes,
     vq_abi_version,
     vq_debug_dequant,
@@ -35,6 +41,7 @@ from ._binding import (  # noqa: F401
     vq_linear_create,
     vq_linear_destroy,
     vq_linear_forward,
+    vq_linear_forward_epilogue,
     vq_linear_forward_noalloc,
     vq_linear_forward_rotated,
     vq_linear_launches,

@@ -23,6 +23,7 @@ VQ_FMT_RVQ12, VQ_FMT_RVQ12_4, VQ_FMT_VQ16, VQ_FMT_VQ16_RVQ = 1, 2, 3, 4
 # including the primary, 8-bit stages after them).
 LADDER_STAGES = {2: (1, 0), 3: (1, 1), 4: (2, 0), 5: (2, 1), 6: (3, 0), 7: (3, 1), 8: (4, 0)}
 VQ_F16, VQ_BF16 = 0, 1
+VQ_ACT_NONE, VQ_ACT_RELU, VQ_ACT_SILU, VQ_ACT_GELU, VQ_ACT_GELU_TANH = range(5)
 VQ_PATH_AUTO, VQ_PATH_LUT, VQ_PATH_GEMV, VQ_PATH_TC, VQ_PATH_GATHER = 0, 1, 2, 3, 4
 
 STATUS_NAMES = {0: "VQ_OK", 1: "VQ_ERR_INVALID_ARG", 2: "VQ_ERR_UNSUPPORTED", 3: "VQ_ERR_CUDA",
@@ -32,7 +33,8 @@ STATUS_NAMES = {0: "VQ_OK", 1: "VQ_ERR_INVALID_ARG", 2: "VQ_ERR_UNSUPPORTED", 3:
 EXPORTS = ("vq_abi_version", "vq_linear_create", "vq_linear_destroy", "vq_linear_set_path", "vq_linear_set_sm_budget",
            "vq_linear_forward",
            "vq_linear_forward_noalloc", "vq_linear_forward_rotated", "vq_linear_launches", "vq_linear_plan", "vq_plan_for_device", "vq_rht_apply", "vq_rht_apply_output", "vq_rht_apply_output_sharded", "vq_encode", "vq_linear_check", "vq_last_error",
-           "vq_debug_unpack", "vq_debug_dequant", "vq_debug_wait_timeout")
+           "vq_debug_unpack", "vq_debug_dequant", "vq_debug_wait_timeout",
+           "vq_linear_forward_epilogue")
 
 
 class VQError(RuntimeError):
@@ -62,6 +64,11 @@ class vq_plan_info(ctypes.Structure):
 class vq_codebooks(ctypes.Structure):
     _fields_ = [("cb1", ctypes.c_void_p), ("cb2", ctypes.c_void_p), ("cbr", ctypes.c_void_p * 3),
                 ("cb8", ctypes.c_void_p)]
+
+
+class vq_epilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -110,6 +117,9 @@ def load(path: str | None = None):
         lib.vq_linear_forward_rotated.restype = st
         lib.vq_linear_forward_rotated.argtypes = [P, P, P, ctypes.POINTER(vq_planes), ctypes.POINTER(vq_codebooks), P,
                                                   P, I32, I32, I32, P]
+        lib.vq_linear_forward_epilogue.restype = st
+        lib.vq_linear_forward_epilogue.argtypes = [P, P, P, ctypes.POINTER(vq_planes), ctypes.POINTER(vq_codebooks), P,
+                                                   ctypes.POINTER(vq_epilogue), P, I32, I32, I32, P]
         lib.vq_rht_apply.restype = st
         lib.vq_rht_apply.argtypes = [P, P, P, I32, I32, I32, P]
         lib.vq_rht_apply_output.restype = st
@@ -228,6 +238,18 @@ def vq_linear_forward_rotated(h, x, signs, planes: vq_planes, codebooks: vq_code
     """y = rotate(x) . W^T with the rotation's +-1 `signs` (int8 device tensor [K])."""
     _check(load().vq_linear_forward_rotated(h, _ptr(x), _ptr(signs), ctypes.byref(planes), ctypes.byref(codebooks),
                                             _ptr(scales), _ptr(y), M, N, K, _stream(stream)))
+
+
+def make_epilogue(act=VQ_ACT_NONE, bias=None, mul=None, residual=None) -> vq_epilogue:
+    """act(f + bias) * mul + residual; bias [N], mul and residual [M, N], each may be None."""
+    return vq_epilogue(act, _ptr(bias), _ptr(mul), _ptr(residual))
+
+
+def vq_linear_forward_epilogue(h, x, planes: vq_planes, codebooks: vq_codebooks, scales, epilogue: vq_epilogue, y, M,
+                               N, K, signs=None, stream=None) -> None:
+    """vq_linear_forward (with `signs`: vq_linear_forward_rotated) with a fused epilogue."""
+    _check(load().vq_linear_forward_epilogue(h, _ptr(x), _ptr(signs), planes, codebooks, _ptr(scales), epilogue,
+                                             _ptr(y), M, N, K, _stream(stream)))
 
 
 def vq_linear_forward_noalloc(N, K, fmt, scale_group, act_dtype, x, planes: vq_planes, codebooks: vq_codebooks,

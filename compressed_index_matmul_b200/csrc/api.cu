@@ -9,14 +9,12 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
-#include <string>
 
+#include "api_util.h"
 #include "internal.h"
 #include "tools.h"
 #include "vqlinear.h"
 #include "vqlinear_tools.h"
-
-#define VQ_API extern "C" __attribute__((visibility("default")))
 
 namespace vq {
 void plan_gemv(const vq_linear_desc& d, const DeviceInfo& dev, int M, Plan* p);
@@ -41,17 +39,15 @@ struct vq_linear_s {
   float* corr_y;      // the sparse correction's x . C^T, fp32 [max_M][N] (desc.corr == 1)
 };
 
-namespace {
+namespace vq {
 
-thread_local std::string t_err;
+static thread_local char t_err[512];
 
 vq_status fail(vq_status st, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(t_err, sizeof t_err, fmt, ap);
   va_end(ap);
-  t_err = buf;
   return st;
 }
 
@@ -176,10 +172,6 @@ vq::LayerArgs make_args(const vq_linear_desc& d, const vq_planes* p, const vq_co
   return a;
 }
 
-}  // namespace
-
-namespace vq {
-
 bool plan_forward(const vq_linear_desc& d, const DeviceInfo& dev, int M, int forced_path, Plan* out) {
   int path = forced_path;
   if (path == VQ_PATH_AUTO) {
@@ -218,9 +210,11 @@ bool plan_forward(const vq_linear_desc& d, const DeviceInfo& dev, int M, int for
 
 }  // namespace vq
 
+using namespace vq;
+
 VQ_API int32_t vq_abi_version(void) { return 3; }
 
-VQ_API const char* vq_last_error(void) { return t_err.c_str(); }
+VQ_API const char* vq_last_error(void) { return vq::t_err; }
 
 VQ_API vq_status vq_linear_create(const vq_linear_desc* desc, vq_linear_t* out) {
   if (out == nullptr) return fail(VQ_ERR_INVALID_ARG, "out is NULL");
@@ -403,21 +397,26 @@ VQ_API vq_status vq_plan_for_device(const vq_linear_desc* desc, int32_t M, int32
   return VQ_OK;
 }
 
-VQ_API vq_status vq_linear_forward(vq_linear_t h, const void* x, const vq_planes* planes,
-                                   const vq_codebooks* codebooks, const void* scales, void* y, int32_t M,
-                                   int32_t N, int32_t K, void* stream) {
-  if (h == nullptr) return fail(VQ_ERR_INVALID_ARG, "handle is NULL");
+namespace {
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+void set_epilogue(vq::LayerArgs& a, const vq_epilogue* epi) {
+  if (!epi) return;
+  a.bias = static_cast<const uint16_t*>(epi->bias);
+  a.mul = static_cast<const uint16_t*>(epi->mul);
+  a.res = static_cast<const uint16_t*>(epi->residual);
+  a.act_fn = epi->act;
+  a.epi = epi->act != VQ_ACT_NONE || epi->bias || epi->mul || epi->residual;
+}
+
+// One forward, its arguments checked; `epi` may be NULL.
+vq_status run_forward(vq_linear_t h, const void* x, const vq_planes* planes, const vq_codebooks* codebooks,
+                      const void* scales, const vq_epilogue* epi, void* y, int32_t M, cudaStream_t s) {
   const vq_linear_desc& d = h->d;
-  if (N != d.N || K != d.K)
-    return fail(VQ_ERR_INVALID_ARG, "N=%d, K=%d do not match the handle's N=%d, K=%d", N, K, d.N, d.K);
-  if (M < 0 || M > d.max_M) return fail(VQ_ERR_INVALID_ARG, "M=%d outside [0, max_M=%d]", M, d.max_M);
-  vq_status st;
-  if ((st = check_ptr(x, "x")) || (st = check_ptr(y, "y")) || (st = validate_planes(d, planes)) ||
-      (st = validate_codebooks(d, codebooks, scales)))
-    return st;
-  if (x == y) return fail(VQ_ERR_INVALID_ARG, "y must not alias x");
-  if (M == 0) return VQ_OK;
-  if ((st = check_device(h))) return st;
   vq::Plan p{};
   if (!vq::plan_forward(d, h->dev, M, h->path, &p))
     return fail(VQ_ERR_UNSUPPORTED, "path %d cannot run M=%d", h->path, M);
@@ -430,7 +429,7 @@ VQ_API vq_status vq_linear_forward(vq_linear_t h, const void* x, const vq_planes
   a.x = x;
   a.y = y;
   a.M = M;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  set_epilogue(a, epi);
   cudaError_t e;
   if (d.corr) {  // x . C^T first, in fp32; the forward kernel adds it before rounding
     e = vq::launch_corr(a, h->corr_y, s);
@@ -447,27 +446,14 @@ VQ_API vq_status vq_linear_forward(vq_linear_t h, const void* x, const vq_planes
   return VQ_OK;
 }
 
-VQ_API vq_status vq_linear_forward_rotated(vq_linear_t h, const void* x, const int8_t* signs, const vq_planes* planes,
-                                           const vq_codebooks* codebooks, const void* scales, void* y, int32_t M,
-                                           int32_t N, int32_t K, void* stream) {
-  if (h == nullptr) return fail(VQ_ERR_INVALID_ARG, "handle is NULL");
+// The rotated forward, its arguments checked; `epi` may be NULL.
+vq_status run_forward_rotated(vq_linear_t h, const void* x, const int8_t* signs, const vq_planes* planes,
+                              const vq_codebooks* codebooks, const void* scales, const vq_epilogue* epi, void* y,
+                              int32_t M, int32_t K, cudaStream_t s) {
   const vq_linear_desc& d = h->d;
-  if (N != d.N || K != d.K)
-    return fail(VQ_ERR_INVALID_ARG, "N=%d, K=%d do not match the handle's N=%d, K=%d", N, K, d.N, d.K);
-  if (K < 64 || K > 32768 || K % 64 != 0)
-    return fail(VQ_ERR_INVALID_ARG, "K=%d: the rotation needs a multiple of 64 in [64, 32768]", K);
-  if (M < 0 || M > d.max_M) return fail(VQ_ERR_INVALID_ARG, "M=%d outside [0, max_M=%d]", M, d.max_M);
-  vq_status st;
-  if ((st = check_ptr(signs, "signs")) || (st = check_ptr(x, "x")) || (st = check_ptr(y, "y")) || (st = validate_planes(d, planes)) ||
-      (st = validate_codebooks(d, codebooks, scales)))
-    return st;
-  if (x == y) return fail(VQ_ERR_INVALID_ARG, "y must not alias x");
-  if (M == 0) return VQ_OK;
-  if ((st = check_device(h))) return st;
   vq::Plan p{};
   if (!vq::plan_forward(d, h->dev, M, h->path, &p))
     return fail(VQ_ERR_UNSUPPORTED, "path %d cannot run M=%d", h->path, M);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   // Where the forward runs the 16-bit gather kernel (automatically up to M = 4, or
   // forced up to M = 8) that kernel rotates x itself: one launch, no rotated copy of
   // x in memory.  (A sparse correction needs the rotated x too: that layer takes the
@@ -481,6 +467,7 @@ VQ_API vq_status vq_linear_forward_rotated(vq_linear_t h, const void* x, const i
     a.x = x;
     a.y = y;
     a.M = M;
+    set_epilogue(a, epi);
     cudaError_t e = vq::launch_vq16(a, p, signs, s);
     if (e != cudaSuccess) return cuda_fail(e, "vq_linear_forward_rotated launch");
     return VQ_OK;
@@ -490,7 +477,79 @@ VQ_API vq_status vq_linear_forward_rotated(vq_linear_t h, const void* x, const i
                 "this shape's rotation is not fused and the handle has no rotation buffer (create it with rht = 1)");
   cudaError_t e = vq::launch_rht(x, h->xrot, signs, M, K, d.act_dtype, s);
   if (e != cudaSuccess) return cuda_fail(e, "vq_linear_forward_rotated rotation launch");
-  return vq_linear_forward(h, h->xrot, planes, codebooks, scales, y, M, N, K, stream);
+  return run_forward(h, h->xrot, planes, codebooks, scales, epi, y, M, s);
+}
+
+// The argument checks of the forwards of a handle; `signs` is looked at when `rotated`.
+vq_status check_forward(vq_linear_t h, const void* x, bool rotated, const int8_t* signs, const vq_planes* planes,
+                        const vq_codebooks* codebooks, const void* scales, const void* y, int32_t M, int32_t N,
+                        int32_t K) {
+  if (h == nullptr) return fail(VQ_ERR_INVALID_ARG, "handle is NULL");
+  const vq_linear_desc& d = h->d;
+  if (N != d.N || K != d.K)
+    return fail(VQ_ERR_INVALID_ARG, "N=%d, K=%d do not match the handle's N=%d, K=%d", N, K, d.N, d.K);
+  if (rotated && (K < 64 || K > 32768 || K % 64 != 0))
+    return fail(VQ_ERR_INVALID_ARG, "K=%d: the rotation needs a multiple of 64 in [64, 32768]", K);
+  if (M < 0 || M > d.max_M) return fail(VQ_ERR_INVALID_ARG, "M=%d outside [0, max_M=%d]", M, d.max_M);
+  vq_status st;
+  if (rotated && (st = check_ptr(signs, "signs"))) return st;
+  if ((st = check_ptr(x, "x")) || (st = check_ptr(y, "y")) || (st = validate_planes(d, planes)) ||
+      (st = validate_codebooks(d, codebooks, scales)))
+    return st;
+  if (x == y) return fail(VQ_ERR_INVALID_ARG, "y must not alias x");
+  return VQ_OK;
+}
+
+}  // namespace
+
+VQ_API vq_status vq_linear_forward(vq_linear_t h, const void* x, const vq_planes* planes,
+                                   const vq_codebooks* codebooks, const void* scales, void* y, int32_t M,
+                                   int32_t N, int32_t K, void* stream) {
+  vq_status st = check_forward(h, x, false, nullptr, planes, codebooks, scales, y, M, N, K);
+  if (st) return st;
+  if (M == 0) return VQ_OK;
+  if ((st = check_device(h))) return st;
+  return run_forward(h, x, planes, codebooks, scales, nullptr, y, M, static_cast<cudaStream_t>(stream));
+}
+
+VQ_API vq_status vq_linear_forward_rotated(vq_linear_t h, const void* x, const int8_t* signs, const vq_planes* planes,
+                                           const vq_codebooks* codebooks, const void* scales, void* y, int32_t M,
+                                           int32_t N, int32_t K, void* stream) {
+  vq_status st = check_forward(h, x, true, signs, planes, codebooks, scales, y, M, N, K);
+  if (st) return st;
+  if (M == 0) return VQ_OK;
+  if ((st = check_device(h))) return st;
+  return run_forward_rotated(h, x, signs, planes, codebooks, scales, nullptr, y, M, K,
+                             static_cast<cudaStream_t>(stream));
+}
+
+VQ_API vq_status vq_linear_forward_epilogue(vq_linear_t h, const void* x, const int8_t* signs,
+                                            const vq_planes* planes, const vq_codebooks* codebooks,
+                                            const void* scales, const vq_epilogue* epi, void* y, int32_t M, int32_t N,
+                                            int32_t K, void* stream) {
+  const bool rotated = signs != nullptr;
+  vq_status st = check_forward(h, x, rotated, signs, planes, codebooks, scales, y, M, N, K);
+  if (st) return st;
+  if (epi == nullptr) return fail(VQ_ERR_INVALID_ARG, "epi is NULL");
+  if (epi->act < VQ_ACT_NONE || epi->act > VQ_ACT_GELU_TANH)
+    return fail(VQ_ERR_INVALID_ARG, "epi->act=%d is not a VQ_ACT_*", epi->act);
+  const struct {
+    const void* p;
+    const char* name;
+  } parts[3] = {{epi->bias, "epi->bias"}, {epi->mul, "epi->mul"}, {epi->residual, "epi->residual"}};
+  for (const auto& q : parts)
+    if (q.p && (st = check_ptr(q.p, q.name))) return st;
+  const size_t ybytes = (size_t)M * N * 2;
+  if (overlaps(x, (size_t)M * K * 2, y, ybytes)) return fail(VQ_ERR_INVALID_ARG, "y overlaps x");
+  if (epi->bias && overlaps(epi->bias, (size_t)N * 2, y, ybytes)) return fail(VQ_ERR_INVALID_ARG, "y overlaps epi->bias");
+  for (int i = 1; i < 3; ++i)
+    if (parts[i].p && parts[i].p != y && overlaps(parts[i].p, ybytes, y, ybytes))
+      return fail(VQ_ERR_INVALID_ARG, "y partially overlaps %s", parts[i].name);
+  if (M == 0) return VQ_OK;
+  if ((st = check_device(h))) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return rotated ? run_forward_rotated(h, x, signs, planes, codebooks, scales, epi, y, M, K, s)
+                 : run_forward(h, x, planes, codebooks, scales, epi, y, M, s);
 }
 
 VQ_API vq_status vq_rht_apply(const void* x, void* x_out, const int8_t* signs, int32_t M, int32_t K, int32_t dtype,

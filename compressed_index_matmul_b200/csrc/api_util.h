@@ -1,0 +1,22 @@
+// Host-side helpers shared by the C ABI's translation units: error reporting and the
+// argument checks (api.cu defines them).
+#pragma once
+
+#include "internal.h"
+
+#define VQ_API extern "C" __attribute__((visibility("default")))
+
+namespace vq {
+
+// Record the calling thread's message and return the status.
+vq_status fail(vq_status st, const char* fmt, ...);
+vq_status cuda_fail(cudaError_t e, const char* what);
+
+bool aligned16(const void* p);
+vq_status check_ptr(const void* p, const char* name);
+vq_status validate_desc(const vq_linear_desc* d);
+vq_status validate_planes(const vq_linear_desc& d, const vq_planes* p);
+vq_status validate_codebooks(const vq_linear_desc& d, const vq_codebooks* cb, const void* scales);
+LayerArgs make_args(const vq_linear_desc& d, const vq_planes* p, const vq_codebooks* cb, const void* scales);
+
+}  // namespace vq

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "vqlinear.h"
+#include "vqlinear_ffn.h"
 
 namespace vq {
 
@@ -37,6 +38,12 @@ struct LayerArgs {
   const int32_t* corr_cols;
   const uint16_t* corr_vals;
   const float* addend;
+  // The fused epilogue (epilogue.cuh); epi == 0: none, and the pointers are not read.
+  int epi;
+  int act_fn;            // VQ_ACT_*
+  const uint16_t* bias;  // [N] or NULL
+  const uint16_t* mul;   // [M][N] or NULL
+  const uint16_t* res;   // [M][N] or NULL
 };
 
 // Work split chosen for one forward.

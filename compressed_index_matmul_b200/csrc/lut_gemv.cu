@@ -40,6 +40,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
 
@@ -372,8 +373,7 @@ __global__ void __launch_bounds__(kLutThreads, 1)
         }
         if (S == 1) {
           if (!block_scales) acc *= f16_bits_to_f32(a.scales[r]);
-          if (a.addend) acc += a.addend[r];  // the sparse correction's x . C^T term
-          static_cast<uint16_t*>(a.y)[r] = Elt<T>::from_f32(acc);
+          static_cast<uint16_t*>(a.y)[r] = Elt<T>::from_f32(finish<T>(a, r, r, acc));
         } else {
           partial[(int64_t)s * N + r] = acc;
         }
@@ -479,10 +479,8 @@ __global__ void __launch_bounds__(kLutThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o4[i] *= f16_bits_to_f32(a.scales[r + i]);
       }
-      if (a.addend) {  // the sparse correction's x . C^T term
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o4[i] += a.addend[r + i];
-      }
+      for (int i = 0; i < 4; ++i) o4[i] = finish<T>(a, r + i, r + i, o4[i]);
       uint16_t* yr = static_cast<uint16_t*>(a.y) + r;
       *reinterpret_cast<uint2*>(yr) =
           make_uint2((uint32_t)Elt<T>::from_f32(o4[0]) | ((uint32_t)Elt<T>::from_f32(o4[1]) << 16),

@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "internal.h"
 #include "ladder.cuh"
 #include "tc_ptx.cuh"
@@ -444,17 +445,20 @@ __global__ void __launch_bounds__(tc_threads(kTcParts), kTcParts == 2 ? 2 : 1)
         uint32_t v[16];
         ptx::tmem_ld16(taddr + 16 * ci, v);
         ptx::tmem_wait_ld();
+        float f[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          float f = __uint_as_float(v[i]);
+          f[i] = __uint_as_float(v[i]);
           if (pair) {  // two splits: the sum does not depend on the order
             float o;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(o) : "r"(recv_addr(ci, i)));
-            f += o;
+            f[i] += o;
           }
-          // the sparse correction's x . C^T term, added before the one rounding
-          if (a.addend && valid && tok0 + 16 * ci + i < M) f += a.addend[(int64_t)(tok0 + 16 * ci + i) * N + r];
-          const uint16_t h = Elt<T>::from_f32(f);
+        }
+        if (valid) finish16<T>(a, tok0 + 16 * ci, r, f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint16_t h = Elt<T>::from_f32(f[i]);
           asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage_addr(ci, i)), "h"(h) : "memory");
         }
       }
@@ -479,15 +483,18 @@ __global__ void __launch_bounds__(tc_threads(kTcParts), kTcParts == 2 ? 2 : 1)
         uint32_t v[16];
         ptx::tmem_ld16(taddr + c0, v);
         ptx::tmem_wait_ld();
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+        if (p.splits == 1 && valid) finish16<T>(a, tok0 + c0, r, f);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int tok = tok0 + c0 + i;
           if (tok >= M || !valid) continue;
           if (p.splits == 1)
-            y[(int64_t)tok * N + r] =
-                Elt<T>::from_f32(a.addend ? __uint_as_float(v[i]) + a.addend[(int64_t)tok * N + r] : __uint_as_float(v[i]));
+            y[(int64_t)tok * N + r] = Elt<T>::from_f32(f[i]);
           else
-            p.partial[((int64_t)split * M + tok) * N + r] = __uint_as_float(v[i]);
+            p.partial[((int64_t)split * M + tok) * N + r] = f[i];
         }
       }
       ptx::tc_fence_before();
@@ -519,11 +526,10 @@ __global__ void __launch_bounds__(tc_threads(kTcParts), kTcParts == 2 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[i] = k == 0 ? __uint_as_float(t[i]) : acc[i] + __uint_as_float(t[i]);
           }
+          if (valid) finish16<T>(a, tok0 + c0, r, acc);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (valid && tok0 + c0 + i < M)
-              y[(int64_t)(tok0 + c0 + i) * N + r] =
-                  Elt<T>::from_f32(a.addend ? acc[i] + a.addend[(int64_t)(tok0 + c0 + i) * N + r] : acc[i]);
+            if (valid && tok0 + c0 + i < M) y[(int64_t)(tok0 + c0 + i) * N + r] = Elt<T>::from_f32(acc[i]);
         }
         ptx::tc_fence_before();
         if (threadIdx.x == 64) p.tickets[tile] = 0u;

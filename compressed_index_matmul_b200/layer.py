@@ -16,6 +16,22 @@ def _dev(a: np.ndarray, device):
     return torch.from_numpy(a).to(device)
 
 
+def _raw_stream(stream, index):
+    """The raw handle of `stream`, or of the current stream of device `index`."""
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def check_tensor(t, name, shape, dtype, device):
+    """Raise ValueError unless `t` is a contiguous tensor of this shape, type and device."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}: got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}, strides {list(t.stride())}")
+
+
 class VQLinear:
     """Holds the planes, codebooks and scales of one layer in device memory.
 
@@ -34,6 +50,8 @@ class VQLinear:
 
         self.N, self.K, self.fmt, self.scale_group, self.act_dtype, self.max_M = N, K, fmt, scale_group, act_dtype, max_M
         self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.t = {k: _dev(v, self.device) for k, v in arrays.items() if v is not None and k in
                   ("lo", "hi4", "s2", "idx16", "idx8", "cb1", "cb2", "cbr", "cb8", "scales")}
         self.n16, self.n8, self.mult = 0, 0, ()
@@ -89,6 +107,35 @@ class VQLinear:
             y = torch.empty((M, self.N), dtype=self.torch_dtype, device=self.device)
         B.vq_linear_forward_rotated(self.handle, x, signs, self.planes, self.codebooks, self.t["scales"], y, M, self.N,
                                     self.K, stream)
+        return y
+
+    def forward_fused(self, x, act=B.VQ_ACT_NONE, bias=None, mul=None, residual=None, signs=None, y=None, stream=None):
+        """y = act(x . W^T + bias) * mul + residual in one forward (vq_linear_forward_epilogue).
+
+        x [M, K], bias [N], mul and residual [M, N] are contiguous tensors of the layer's
+        type on its device, each of the last three may be None; mul and residual may be `y`
+        itself (``forward_fused(x, residual=h, y=h)`` adds to h in place).  `act` is a VQ_ACT_*.
+        With `signs` (int8 [K]) x is rotated first, as by ``forward_rotated``."""
+        import torch
+
+        dt, dev, M, N = self.torch_dtype, self.device, x.shape[0], self.N
+        check_tensor(x, "x", (M, self.K), dt, dev)
+        if bias is not None:
+            check_tensor(bias, "bias", (N,), dt, dev)
+        if mul is not None:
+            check_tensor(mul, "mul", (M, N), dt, dev)
+        if residual is not None:
+            check_tensor(residual, "residual", (M, N), dt, dev)
+        if signs is not None:
+            check_tensor(signs, "signs", (self.K,), torch.int8, dev)
+        if y is None:
+            y = torch.empty((M, N), dtype=dt, device=dev)
+        else:
+            check_tensor(y, "y", (M, N), dt, dev)
+        if M > 0:
+            B.vq_linear_forward_epilogue(self.handle, x, self.planes, self.codebooks, self.t["scales"],
+                                         B.make_epilogue(act, bias, mul, residual), y, M, N, self.K, signs,
+                                         _raw_stream(stream, dev.index))
         return y
 
     def set_path(self, path: int):

@@ -1,0 +1,84 @@
+"""Host-side checks of the feed-forward entry points that need no GPU."""
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+from compressed_index_matmul_b200 import _binding as B
+from compressed_index_matmul_b200 import build as libbuild
+from compressed_index_matmul_b200.layer import VQLinear, check_tensor
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    libbuild.build()
+    return B.load()
+
+
+def c_layout(tmp_path, structs):
+    """sizeof and offsetof of the ABI structs as gcc lays them out from the header."""
+    src = ["#include <stddef.h>", "#include <stdio.h>", '#include "vqlinear_ffn.h"', "int main(void) {"]
+    for st, fs in structs.items():
+        src.append(f'  printf("{st} sizeof %zu\\n", sizeof({st}));')
+        src += [f'  printf("{st} {f} %zu\\n", offsetof({st}, {f}));' for f in fs]
+    (tmp_path / "o.c").write_text("\n".join(src + ["  return 0;\n}"]))
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(tmp_path / "o.c"), "-o",
+                    str(tmp_path / "o")], check=True)
+    out = subprocess.run([str(tmp_path / "o")], capture_output=True, text=True, check=True).stdout
+    return {(a, b): int(c) for a, b, c in (ln.split() for ln in out.splitlines())}
+
+
+def same_layout(tmp_path, names):
+    structs = {n: [f for f, _ in getattr(B, n)._fields_] for n in names}
+    got = c_layout(tmp_path, structs)
+    for st, fs in structs.items():
+        cls = getattr(B, st)
+        assert got[(st, "sizeof")] == ctypes.sizeof(cls), st
+        for f in fs:
+            assert got[(st, f)] == getattr(cls, f).offset, (st, f)
+
+
+def test_epilogue_struct_matches_the_header(tmp_path):
+    same_layout(tmp_path, ["vq_epilogue"])
+
+
+def test_epilogue_rejects_a_null_handle(lib):
+    e = B.make_epilogue()
+    cb, pl = B.make_codebooks(16, 16), B.make_planes(16, 16, 16)
+    assert lib.vq_linear_forward_epilogue(None, 16, None, pl, cb, 16, e, 16, 1, 64, 64, None) == B.VQ_ERR_INVALID_ARG
+    assert b"handle" in lib.vq_last_error()
+
+
+def test_long_messages_are_cut_not_lost(lib):
+    assert lib.vq_rht_apply(16, 16, 16, 1, 100, 0, None) == B.VQ_ERR_INVALID_ARG
+    assert 0 < len(lib.vq_last_error()) < 512
+
+
+def test_check_tensor():
+    cpu = torch.device("cpu")
+    t = torch.zeros((4, 8), dtype=torch.float16)
+    check_tensor(t, "t", (4, 8), torch.float16, cpu)
+    for bad in (t[:, ::2], t.t(), t.float(), t[:3]):
+        with pytest.raises(ValueError, match="t must be a contiguous"):
+            check_tensor(bad, "t", (4, 8), torch.float16, cpu)
+    with pytest.raises(ValueError):
+        check_tensor(t, "t", (4, 8), torch.float16, torch.device("meta"))
+
+
+def test_fused_forward_checks_its_tensors_before_the_library():
+    """No handle is needed to refuse a tensor of another shape, type or layout."""
+    L = VQLinear.__new__(VQLinear)
+    L.N, L.K, L.act_dtype, L.device, L.handle = 16, 64, B.VQ_F16, torch.device("cpu"), None
+    x = torch.zeros((2, 64), dtype=torch.float16)
+    y = torch.zeros((2, 16), dtype=torch.float16)
+    for kw, name in ((dict(bias=y), "bias"), (dict(mul=y[:1]), "mul"), (dict(residual=y.float()), "residual"),
+                     (dict(y=y.t()), "y"), (dict(signs=y[0]), "signs")):
+        with pytest.raises(ValueError, match=f"{name} must be"):
+            L.forward_fused(x, **kw)
+    with pytest.raises(ValueError, match="x must be"):
+        L.forward_fused(x[:, :32])
