@@ -5,6 +5,7 @@ The compute lives in ``libvqlinear.so`` (CUDA kernels behind the C ABI declared 
 
 * ``_binding``  -- ctypes binding with the C ABI's names
 * ``layer``     -- ``VQLinear``: one layer's device tensors plus a handle
+* ``moe``       -- ``VQRouter`` and ``combine``: tokens to experts and back
 * ``build``     -- compiles the library in-tree with nvcc
 """
 
@@ -17,6 +18,7 @@ from ._binding import (  # noqa: F401
     VQ_ACT_SILU,
     VQ_BF16,
     VQ_F16,
+    VQ_F32,
     VQ_FMT_RVQ12,
     VQ_FMT_RVQ12_4,
     VQ_FMT_VQ16,
@@ -37,6 +39,7 @@ from ._binding import (  # noqa: F401
     vq_debug_unpack,
     vq_debug_wait_timeout,
     vq_encode,
+    vq_experts_combine,
     vq_linear_check,
     vq_linear_create,
     vq_linear_destroy,
@@ -52,5 +55,9 @@ from ._binding import (  # noqa: F401
     vq_rht_apply,
     vq_rht_apply_output,
     vq_rht_apply_output_sharded,
+    vq_router_create,
+    vq_router_destroy,
+    vq_router_forward,
 )
 from .layer import VQLinear  # noqa: F401
+from .moe import VQRouter, VQRouting, combine  # noqa: F401

@@ -22,7 +22,7 @@ VQ_FMT_RVQ12, VQ_FMT_RVQ12_4, VQ_FMT_VQ16, VQ_FMT_VQ16_RVQ = 1, 2, 3, 4
 # GLQ README, "Bit widths": bits per weight of the residual ladder -> (16-bit stages
 # including the primary, 8-bit stages after them).
 LADDER_STAGES = {2: (1, 0), 3: (1, 1), 4: (2, 0), 5: (2, 1), 6: (3, 0), 7: (3, 1), 8: (4, 0)}
-VQ_F16, VQ_BF16 = 0, 1
+VQ_F16, VQ_BF16, VQ_F32 = 0, 1, 2
 VQ_ACT_NONE, VQ_ACT_RELU, VQ_ACT_SILU, VQ_ACT_GELU, VQ_ACT_GELU_TANH = range(5)
 VQ_PATH_AUTO, VQ_PATH_LUT, VQ_PATH_GEMV, VQ_PATH_TC, VQ_PATH_GATHER = 0, 1, 2, 3, 4
 
@@ -34,7 +34,8 @@ EXPORTS = ("vq_abi_version", "vq_linear_create", "vq_linear_destroy", "vq_linear
            "vq_linear_forward",
            "vq_linear_forward_noalloc", "vq_linear_forward_rotated", "vq_linear_launches", "vq_linear_plan", "vq_plan_for_device", "vq_rht_apply", "vq_rht_apply_output", "vq_rht_apply_output_sharded", "vq_encode", "vq_linear_check", "vq_last_error",
            "vq_debug_unpack", "vq_debug_dequant", "vq_debug_wait_timeout",
-           "vq_linear_forward_epilogue")
+           "vq_linear_forward_epilogue", "vq_router_create", "vq_router_destroy", "vq_router_forward",
+           "vq_experts_combine")
 
 
 class VQError(RuntimeError):
@@ -69,6 +70,10 @@ class vq_codebooks(ctypes.Structure):
 class vq_epilogue(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p),
                 ("residual", ctypes.c_void_p)]
+
+
+class vq_router_desc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("k", ctypes.c_int32), ("renorm", ctypes.c_int32), ("max_T", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -120,6 +125,14 @@ def load(path: str | None = None):
         lib.vq_linear_forward_epilogue.restype = st
         lib.vq_linear_forward_epilogue.argtypes = [P, P, P, ctypes.POINTER(vq_planes), ctypes.POINTER(vq_codebooks), P,
                                                    ctypes.POINTER(vq_epilogue), P, I32, I32, I32, P]
+        lib.vq_router_create.restype = st
+        lib.vq_router_create.argtypes = [ctypes.POINTER(vq_router_desc), ctypes.POINTER(P)]
+        lib.vq_router_destroy.restype = st
+        lib.vq_router_destroy.argtypes = [P]
+        lib.vq_router_forward.restype = st
+        lib.vq_router_forward.argtypes = [P, P, I32, P, P, P, P, P, I32, P]
+        lib.vq_experts_combine.restype = st
+        lib.vq_experts_combine.argtypes = [P, I32, P, P, P, P, I32, I32, I32, I32, P]
         lib.vq_rht_apply.restype = st
         lib.vq_rht_apply.argtypes = [P, P, P, I32, I32, I32, P]
         lib.vq_rht_apply_output.restype = st
@@ -250,6 +263,28 @@ def vq_linear_forward_epilogue(h, x, planes: vq_planes, codebooks: vq_codebooks,
     """vq_linear_forward (with `signs`: vq_linear_forward_rotated) with a fused epilogue."""
     _check(load().vq_linear_forward_epilogue(h, _ptr(x), _ptr(signs), planes, codebooks, _ptr(scales), epilogue,
                                              _ptr(y), M, N, K, _stream(stream)))
+
+
+def vq_router_create(E, k, max_T, renorm=0) -> int:
+    h = ctypes.c_void_p()
+    _check(load().vq_router_create(vq_router_desc(E, k, int(renorm), max_T), ctypes.byref(h)))
+    return h.value
+
+
+def vq_router_destroy(h) -> None:
+    _check(load().vq_router_destroy(h))
+
+
+def vq_router_forward(h, logits, dtype, ids, weights, offsets, rows, slots, T, stream=None) -> None:
+    """The k best experts of every token, their weights, and the pairs in expert order."""
+    _check(load().vq_router_forward(h, _ptr(logits), dtype, _ptr(ids), _ptr(weights), _ptr(offsets), _ptr(rows),
+                                    _ptr(slots), T, _stream(stream)))
+
+
+def vq_experts_combine(y, y_rows, weights, slots, residual, out, T, k, N, dtype, stream=None) -> None:
+    """out[t] = sum_j weights[t][j] y[slots[t][j]] + residual[t]."""
+    _check(load().vq_experts_combine(_ptr(y), y_rows, _ptr(weights), _ptr(slots), _ptr(residual), _ptr(out), T, k, N,
+                                     dtype, _stream(stream)))
 
 
 def vq_linear_forward_noalloc(N, K, fmt, scale_group, act_dtype, x, planes: vq_planes, codebooks: vq_codebooks,

@@ -129,13 +129,45 @@ vq_status validate_codebooks(const vq_linear_desc& d, const vq_codebooks* cb, co
   return VQ_OK;
 }
 
-vq_status check_device(const vq_linear_s* h) {
+vq_status check_current_device(int device) {
   int cur = -1;
   cudaError_t e = cudaGetDevice(&cur);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (cur != h->dev.device)
-    return fail(VQ_ERR_INVALID_ARG, "current device %d differs from the handle's device %d", cur, h->dev.device);
+  if (cur != device)
+    return fail(VQ_ERR_INVALID_ARG, "current device %d differs from the handle's device %d", cur, device);
   return VQ_OK;
+}
+
+static vq_status check_device(const vq_linear_s* h) { return check_current_device(h->dev.device); }
+
+vq_status query_device(DeviceInfo* dev) {
+  cudaError_t e = cudaGetDevice(&dev->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  int major = 0, minor = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev->device);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev->device);
+  if (major != 10 || minor != 0)
+    return fail(VQ_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a only", dev->device, major,
+                minor);
+  cudaDeviceGetAttribute(&dev->num_sms, cudaDevAttrMultiProcessorCount, dev->device);
+  cudaDeviceGetAttribute(&dev->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev->device);
+  return VQ_OK;
+}
+
+cudaError_t free_on_device(int device, void* a, void* b) {
+  int prev = -1;
+  cudaError_t e = cudaGetDevice(&prev);
+  if (e == cudaSuccess && prev != device) e = cudaSetDevice(device);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess && a) e = cudaFree(a);
+  if (e == cudaSuccess && b) e = cudaFree(b);
+  if (prev >= 0 && prev != device) cudaSetDevice(prev);
+  return e;
+}
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
 }
 
 vq::LayerArgs make_args(const vq_linear_desc& d, const vq_planes* p, const vq_codebooks* cb, const void* scales) {
@@ -222,16 +254,8 @@ VQ_API vq_status vq_linear_create(const vq_linear_desc* desc, vq_linear_t* out) 
   vq_status st = validate_desc(desc);
   if (st) return st;
   vq::DeviceInfo dev{};
-  cudaError_t e = cudaGetDevice(&dev.device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev.device);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev.device);
-  if (major != 10 || minor != 0)
-    return fail(VQ_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a only", dev.device,
-                major, minor);
-  cudaDeviceGetAttribute(&dev.num_sms, cudaDevAttrMultiProcessorCount, dev.device);
-  cudaDeviceGetAttribute(&dev.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev.device);
+  cudaError_t e;
+  if ((st = query_device(&dev))) return st;
 
   // Scratch: the largest any path may need for any M <= max_M.
   size_t need = 0;
@@ -398,11 +422,6 @@ VQ_API vq_status vq_plan_for_device(const vq_linear_desc* desc, int32_t M, int32
 }
 
 namespace {
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
 
 void set_epilogue(vq::LayerArgs& a, const vq_epilogue* epi) {
   if (!epi) return;

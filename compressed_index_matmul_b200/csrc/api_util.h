@@ -19,4 +19,12 @@ vq_status validate_planes(const vq_linear_desc& d, const vq_planes* p);
 vq_status validate_codebooks(const vq_linear_desc& d, const vq_codebooks* cb, const void* scales);
 LayerArgs make_args(const vq_linear_desc& d, const vq_planes* p, const vq_codebooks* cb, const void* scales);
 
+// The current device, which must be sm_100.
+vq_status query_device(DeviceInfo* dev);
+vq_status check_current_device(int device);
+// Waits for all work of `device` and frees a and b (either may be NULL) there.
+cudaError_t free_on_device(int device, void* a, void* b = nullptr);
+// Whether the byte ranges [a, a + na) and [b, b + nb) meet.
+bool overlaps(const void* a, size_t na, const void* b, size_t nb);
+
 }  // namespace vq

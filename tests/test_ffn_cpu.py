@@ -43,8 +43,8 @@ def same_layout(tmp_path, names):
             assert got[(st, f)] == getattr(cls, f).offset, (st, f)
 
 
-def test_epilogue_struct_matches_the_header(tmp_path):
-    same_layout(tmp_path, ["vq_epilogue"])
+def test_structs_match_the_header(tmp_path):
+    same_layout(tmp_path, ["vq_epilogue", "vq_router_desc"])
 
 
 def test_epilogue_rejects_a_null_handle(lib):
@@ -82,3 +82,52 @@ def test_fused_forward_checks_its_tensors_before_the_library():
             L.forward_fused(x, **kw)
     with pytest.raises(ValueError, match="x must be"):
         L.forward_fused(x[:, :32])
+
+
+@pytest.mark.parametrize("E,k,max_T,renorm,status", [
+    (0, 1, 1, 0, 1), (4, 0, 1, 0, 1), (4, 5, 1, 0, 1), (513, 1, 1, 0, 2), (64, 33, 1, 0, 2), (4, 1, 0, 0, 1),
+    (4, 1, 1, 2, 1), (64, 32, 1 << 26, 0, 1),
+])
+def test_router_rejects_bad_descriptors(lib, E, k, max_T, renorm, status):
+    h = ctypes.c_void_p(1)
+    assert lib.vq_router_create(B.vq_router_desc(E, k, renorm, max_T), ctypes.byref(h)) == status
+    assert h.value is None and lib.vq_last_error()
+
+
+def test_router_null_arguments(lib):
+    assert lib.vq_router_create(None, None) == B.VQ_ERR_INVALID_ARG
+    h = ctypes.c_void_p()
+    assert lib.vq_router_create(None, ctypes.byref(h)) == B.VQ_ERR_INVALID_ARG
+    assert lib.vq_router_forward(None, 16, 0, 16, 16, 16, 16, 16, 1, None) == B.VQ_ERR_INVALID_ARG
+    assert lib.vq_router_destroy(None) == B.VQ_OK
+
+
+P, Q = 1 << 20, 1 << 24  # addresses that are never read
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), 1), (dict(y_rows=-1), 1), (dict(k=0), 1), (dict(k=33), 1), (dict(N=0), 1), (dict(N=12), 2), (dict(N=1 << 25), 2),
+    (dict(dtype=2), 1), (dict(y=None), 1), (dict(w=None), 1), (dict(slots=None), 1), (dict(out=None), 1), (dict(y=P + 8), 1),
+    (dict(res=Q + 16), 1),       # overlaps out, and is not out
+    (dict(out=P + 64), 1),       # inside y
+    (dict(out=P - 16), 1),       # runs into y
+    (dict(w=Q + 16), 1), (dict(slots=Q), 1),
+])
+def test_combine_rejects_bad_arguments(lib, kw, status):
+    a = dict(y=P, y_rows=8, w=1 << 12, slots=1 << 13, res=None, out=Q, T=4, k=2, N=64, dtype=1)
+    a.update(kw)
+    assert lib.vq_experts_combine(a["y"], a["y_rows"], a["w"], a["slots"], a["res"], a["out"], a["T"], a["k"], a["N"],
+                                  a["dtype"], None) == status
+
+
+def test_combine_of_no_tokens(lib):
+    assert lib.vq_experts_combine(None, 0, None, None, None, None, 0, 2, 64, 1, None) == B.VQ_OK
+
+
+def test_combine_checks_its_tensors():
+    import compressed_index_matmul_b200 as vq
+
+    with pytest.raises(ValueError, match="float16 or bfloat16"):
+        vq.combine(torch.zeros(4, 8), None, None)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        vq.combine(torch.zeros((4, 8), dtype=torch.float16), torch.zeros(2, 2), torch.zeros((2, 2), dtype=torch.int32))
