@@ -5,7 +5,8 @@ The compute lives in ``libvqlinear.so`` (CUDA kernels behind the C ABI declared 
 
 * ``_binding``  -- ctypes binding with the C ABI's names
 * ``layer``     -- ``VQLinear``: one layer's device tensors plus a handle
-* ``moe``       -- ``VQRouter`` and ``combine``: tokens to experts and back
+* ``moe``       -- ``VQExperts``: products grouped by expert; ``VQRouter`` and ``combine``: tokens to
+  experts and back
 * ``build``     -- compiles the library in-tree with nvcc
 """
 
@@ -39,7 +40,13 @@ from ._binding import (  # noqa: F401
     vq_debug_unpack,
     vq_debug_wait_timeout,
     vq_encode,
+    vq_experts_check,
     vq_experts_combine,
+    vq_experts_create,
+    vq_experts_destroy,
+    vq_experts_forward,
+    vq_experts_plan,
+    vq_experts_set_path,
     vq_linear_check,
     vq_linear_create,
     vq_linear_destroy,
@@ -60,4 +67,4 @@ from ._binding import (  # noqa: F401
     vq_router_forward,
 )
 from .layer import VQLinear  # noqa: F401
-from .moe import VQRouter, VQRouting, combine  # noqa: F401
+from .moe import VQExperts, VQRouter, VQRouting, combine  # noqa: F401

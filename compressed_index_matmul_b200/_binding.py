@@ -35,7 +35,8 @@ EXPORTS = ("vq_abi_version", "vq_linear_create", "vq_linear_destroy", "vq_linear
            "vq_linear_forward_noalloc", "vq_linear_forward_rotated", "vq_linear_launches", "vq_linear_plan", "vq_plan_for_device", "vq_rht_apply", "vq_rht_apply_output", "vq_rht_apply_output_sharded", "vq_encode", "vq_linear_check", "vq_last_error",
            "vq_debug_unpack", "vq_debug_dequant", "vq_debug_wait_timeout",
            "vq_linear_forward_epilogue", "vq_router_create", "vq_router_destroy", "vq_router_forward",
-           "vq_experts_combine")
+           "vq_experts_combine", "vq_experts_create", "vq_experts_destroy", "vq_experts_set_path", "vq_experts_plan",
+           "vq_experts_forward", "vq_experts_check")
 
 
 class VQError(RuntimeError):
@@ -70,6 +71,11 @@ class vq_codebooks(ctypes.Structure):
 class vq_epilogue(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p),
                 ("residual", ctypes.c_void_p)]
+
+
+class vq_experts_desc(ctypes.Structure):
+    _fields_ = [("layer", vq_linear_desc), ("E", ctypes.c_int32), ("shared_codebooks", ctypes.c_int32),
+                ("glu", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 class vq_router_desc(ctypes.Structure):
@@ -125,6 +131,19 @@ def load(path: str | None = None):
         lib.vq_linear_forward_epilogue.restype = st
         lib.vq_linear_forward_epilogue.argtypes = [P, P, P, ctypes.POINTER(vq_planes), ctypes.POINTER(vq_codebooks), P,
                                                    ctypes.POINTER(vq_epilogue), P, I32, I32, I32, P]
+        lib.vq_experts_create.restype = st
+        lib.vq_experts_create.argtypes = [ctypes.POINTER(vq_experts_desc), ctypes.POINTER(P)]
+        lib.vq_experts_destroy.restype = st
+        lib.vq_experts_destroy.argtypes = [P]
+        lib.vq_experts_set_path.restype = st
+        lib.vq_experts_set_path.argtypes = [P, I32]
+        lib.vq_experts_plan.restype = st
+        lib.vq_experts_plan.argtypes = [P, I32, ctypes.POINTER(vq_plan_info)]
+        lib.vq_experts_forward.restype = st
+        lib.vq_experts_forward.argtypes = [P, P, I32, P, P, ctypes.POINTER(vq_planes), ctypes.POINTER(vq_codebooks), P,
+                                           P, P, I32, P]
+        lib.vq_experts_check.restype = st
+        lib.vq_experts_check.argtypes = [P, P]
         lib.vq_router_create.restype = st
         lib.vq_router_create.argtypes = [ctypes.POINTER(vq_router_desc), ctypes.POINTER(P)]
         lib.vq_router_destroy.restype = st
@@ -263,6 +282,40 @@ def vq_linear_forward_epilogue(h, x, planes: vq_planes, codebooks: vq_codebooks,
     """vq_linear_forward (with `signs`: vq_linear_forward_rotated) with a fused epilogue."""
     _check(load().vq_linear_forward_epilogue(h, _ptr(x), _ptr(signs), planes, codebooks, _ptr(scales), epilogue,
                                              _ptr(y), M, N, K, _stream(stream)))
+
+
+def vq_experts_create(E, N, K, fmt, scale_group, act_dtype, max_rows, act=VQ_ACT_NONE, glu=0, shared_codebooks=0, n16=0,
+                      n8=0, mult=(), rht=0, corr=0) -> int:
+    d = vq_experts_desc(make_desc(N, K, fmt, scale_group, act_dtype, max_rows, rht, n16, n8, mult, corr), E,
+                        int(shared_codebooks), int(glu), act)
+    h = ctypes.c_void_p()
+    _check(load().vq_experts_create(ctypes.byref(d), ctypes.byref(h)))
+    return h.value
+
+
+def vq_experts_destroy(h) -> None:
+    _check(load().vq_experts_destroy(h))
+
+
+def vq_experts_set_path(h, path: int) -> None:
+    _check(load().vq_experts_set_path(h, path))
+
+
+def vq_experts_plan(h, T: int) -> dict:
+    info = vq_plan_info()
+    _check(load().vq_experts_plan(h, T, ctypes.byref(info)))
+    return {name: getattr(info, name) for name, _ in vq_plan_info._fields_}
+
+
+def vq_experts_forward(h, x, x_rows, rows, offsets, planes: vq_planes, codebooks: vq_codebooks, scales, bias, y, T,
+                       stream=None) -> None:
+    """The products of T rows grouped by expert; `rows` (may be None) names the x row of each."""
+    _check(load().vq_experts_forward(h, _ptr(x), x_rows, _ptr(rows), _ptr(offsets), planes, codebooks, _ptr(scales),
+                                     _ptr(bias), _ptr(y), T, _stream(stream)))
+
+
+def vq_experts_check(h, stream=None) -> None:
+    _check(load().vq_experts_check(h, _stream(stream)))
 
 
 def vq_router_create(E, k, max_T, renorm=0) -> int:

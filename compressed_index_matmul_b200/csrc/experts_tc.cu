@@ -1,0 +1,519 @@
+// Products grouped by expert for many rows per expert (vq_experts_forward): y[r] =
+// act(x[rows[r]] . W_e^T + b) on the tensor cores, W decoded into tensor memory.
+//
+// A persistent block per SM walks tiles of 128 rows of W (glu: 64 gate rows and the 64 up
+// rows that go with them) x up to Tmax rows of x, over all of K.  The tiles of all experts are
+// numbered in expert order (find_tiles) and cut into one contiguous, equal range per block, so
+// a block changes its expert, and with it the codebook in shared memory, once or twice.
+//   warp 0     x: per 64-wide k block, gathers the tile's x rows (TMA tile::gather4, four rows
+//              a copy, 128-byte swizzle) into a ring of S stages
+//   warp 1     allocates TMEM; lane 0 issues tcgen05.mma (M = 128, N = the tile's rows rounded
+//              up to 16, K = 16), A from TMEM, B from shared memory, and commits each stage
+//   warp 2     lane 0: the expert's 12-bit codebook (one bulk copy when it changes) and, per
+//              128-input slice, the tile's index bytes (one contiguous run per plane; glu: two)
+//              into a ring of slots
+//   warps 4..  decode: three per TMEM lane quarter; thread = one row of the tile (its lane).
+//              Block `it` of the block's whole sequence goes to warp it % 3 of every quarter, into A
+//              stage it % S.  After a tile's last block the same threads read the accumulator,
+//              apply bias and activation and store y: consecutive lanes are consecutive
+//              columns, and rows past the expert's last are not written.
+// All rings run on across tiles: while the decode warps store one tile, x and the indices
+// of the next are already on their way.  With Tmax <= 192 the accumulator has two buffers, so
+// the MMAs of the next tile need not wait for the stores either.
+// Every mbarrier wait is bounded; a timeout sets the handle's error word, and the block winds
+// down (waits for its own copies and MMAs, frees TMEM).
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "experts.cuh"
+
+namespace vq {
+
+constexpr int kXtRows = 128;
+constexpr int kXtParts = 3;                            // decode warps per TMEM lane quarter
+constexpr int kXtDecode = 4 * kXtParts;                // decode warps
+constexpr int kXtThreads = 32 * (4 + kXtDecode);
+constexpr int kXtStages = 4;
+constexpr int kXtMaxT = 256;
+constexpr int kXtSlots = 4;                            // index slices in flight
+constexpr uint32_t kXtACols = 32;                      // TMEM columns of one A stage
+constexpr uint32_t kXtIdxHi = 2048, kXtIdxS2 = 3072, kXtIdxSc = 4096, kXtIdxSlot = 4608;
+constexpr uint32_t kXtOffTiles = 65536;                // after the codebook
+constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 16;
+constexpr uint32_t kXtOffIdx = kXtOffBars + 512;
+constexpr uint32_t kXtOffX = (kXtOffIdx + kXtSlots * kXtIdxSlot + 1023) / 1024 * 1024;
+constexpr uint32_t xt_smem(int Tmax) { return kXtOffX + kXtStages * Tmax * 128u + 1024u; }
+static_assert(xt_smem(kXtMaxT) <= 232448, "shared memory of the widest tile");
+
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int c, int r0, int r1, int r2,
+                                            int r3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+
+// One tile: its expert, its place, its x rows.
+struct XtTile {
+  int e, rt, first, n, T;  // first row of y, rows (<= Tmax), n rounded up to 16
+};
+
+template <int FMT, typename T, bool kStaged>
+__global__ void __launch_bounds__(kXtThreads, 1)
+    experts_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ ExpertsArgs a, int Tmax,
+                      int nacc) {
+  extern __shared__ unsigned char smem_raw[];
+  constexpr bool k16 = (FMT == kFmtVq16 || FMT == kFmtVq16Rvq);
+  constexpr bool kLadder = (FMT == kFmtVq16Rvq);
+  constexpr bool kBook = !k16;
+  constexpr bool kTwo = (FMT == kFmtRvq12_4);
+  static_assert(!(kLadder && kStaged), "the residual ladder reads its indices directly");
+  static_assert(kXtStages >= kXtParts, "a stage barrier may be at most one phase behind");
+  constexpr int kSt = kXtStages;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // the swizzle of the x tiles goes by address bits
+  unsigned char* sm = smem_raw + (base - raw);
+  const uint4* cb1s = reinterpret_cast<const uint4*>(sm);
+  ExpertTiles& tiles = *reinterpret_cast<ExpertTiles*>(sm + kXtOffTiles);
+  const uint32_t bar0 = base + kXtOffBars;
+  auto full_a = [&](int s) { return bar0 + 8u * s; };
+  auto full_b = [&](int s) { return bar0 + 8u * (kSt + s); };
+  auto empty = [&](int s) { return bar0 + 8u * (2 * kSt + s); };
+  auto acc_full = [&](int b) { return bar0 + 8u * (3 * kSt + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8u * (3 * kSt + 2 + b); };
+  const uint32_t cb_full = bar0 + 8u * (3 * kSt + 4), cb_empty = cb_full + 8u;
+  auto idx_full = [&](int s) { return cb_empty + 8u + 8u * s; };
+  auto idx_empty = [&](int s) { return cb_empty + 8u + 8u * (kXtSlots + s); };
+  static_assert(8 * (3 * kSt + 6 + 2 * kXtSlots) <= 256, "barriers overlap the flags");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kXtOffBars + 256);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kXtOffBars + 260);
+  int* part_sums = reinterpret_cast<int*>(sm + kXtOffBars + 264);  // 2 per warp
+  static_assert(264 + 8 * kXtThreads / 32 <= 512, "scan area");
+  const uint32_t b_bytes = (uint32_t)Tmax * 128u;
+  auto b_tile = [&](int s) { return base + kXtOffX + b_bytes * s; };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int N = a.w.N, K = a.w.K, G = K / 8;
+  const int nkb = K / 64, nsl = (K + 127) / 128;
+  const int out_tile = a.glu ? kXtRows / 2 : kXtRows;  // columns of y of a tile
+  const int RT = (a.Nout + out_tile - 1) / out_tile;
+  const uint32_t acols = ((uint32_t)Tmax + 31u) & ~31u;
+  const uint32_t acol0 = acols * nacc;  // then the A stages
+  const uint32_t tneed = acol0 + kSt * kXtACols;
+  const uint32_t tcols = tneed <= 256 ? 256u : 512u;
+
+  if (tid == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      ptx::mbar_init(full_a(s), 4);  // one decode warp per TMEM lane quarter
+      ptx::mbar_init(full_b(s), 1);  // the x warp's expect_tx arrival (+ bytes)
+      ptx::mbar_init(empty(s), 1);   // one tcgen05.commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(acc_full(b), 1);
+      ptx::mbar_init(acc_empty(b), kXtDecode);
+    }
+    ptx::mbar_init(cb_full, 1);
+    ptx::mbar_init(cb_empty, kXtDecode);
+    for (int s = 0; s < kXtSlots; ++s) {
+      ptx::mbar_init(idx_full(s), 1);
+      ptx::mbar_init(idx_empty(s), 8);  // the warps that decode the slice's two blocks
+    }
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(smem_u32(tmem_slot), tcols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  find_tiles(a, Tmax, RT, tiles, part_sums, kXtThreads);
+  const int total = tiles.start[a.E];
+  const int ubeg = (int)((int64_t)total * blockIdx.x / gridDim.x), uend = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+
+  // Tile u; `e` walks along (it starts at the range's first expert).
+  int e_walk = ubeg < uend ? expert_of(tiles, a.E, ubeg) : 0;
+  auto tile_of = [&](int u) {
+    while (e_walk + 1 < a.E && u >= tiles.start[e_walk + 1]) ++e_walk;
+    XtTile t;
+    t.e = e_walk;
+    const int beg = tiles.off[e_walk], n = tiles.off[e_walk + 1] - beg, tt = (n + Tmax - 1) / Tmax;
+    const int local = u - tiles.start[e_walk];
+    t.rt = local / tt;
+    const int tk = local - t.rt * tt;
+    t.first = beg + tk * Tmax;
+    t.n = min(Tmax, n - tk * Tmax);
+    t.T = (t.n + 15) & ~15;
+    return t;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ x rows
+    int it = 0;
+    bool ok = true;
+    for (int u = ubeg; ok && u < uend; ++u) {
+      const XtTile t = tile_of(u);
+      // quads lane and lane + 32 of the tile's rows; places past the last row repeat it
+      int r[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int p = t.first + min(4 * (lane + 32 * h) + j, t.n - 1);
+          const int xr = a.rows ? a.rows[p] : p;
+          r[h][j] = (xr >= 0 && xr < a.x_rows) ? xr : 0;  // the epilogue replaces such a row by zeros
+        }
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const int s = it % kSt;
+        if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty(s), ((it / kSt) - 1) & 1, a.err))) ok = false;
+        if (__any_sync(0xffffffffu, !ok)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)t.T * 128u);
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int qd = lane + 32 * h;
+          if (4 * qd < t.T) tma_gather4(b_tile(s) + 512u * qd, &xmap, 64 * kb, r[h][0], r[h][1], r[h][2], r[h][3], full_b(s));
+        }
+      }
+    }
+    // Do not leave while a copy into this block's shared memory may be in flight.
+    for (int i = it > kSt ? it - kSt : 0; i < it; ++i) ptx::mbar_wait(full_b(i % kSt), (i / kSt) & 1, a.err);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kAbFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      bool ok = true;
+      int it = 0, ui = 0, issued = 0;
+      for (int u = ubeg; ok && u < uend; ++u, ++ui) {
+        const XtTile t = tile_of(u);
+        const uint32_t idesc = ptx::idesc_f16(kAbFmt, kXtRows, (uint32_t)t.T);
+        const int b = ui % nacc;
+        const uint32_t acc = tmem + acols * b;
+        // the decode warps have read the buffer's last tile
+        if (*abort_flag || (ui >= nacc && !ptx::mbar_wait(acc_empty(b), ((ui / nacc) - 1) & 1, a.err))) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % kSt;
+          const uint32_t par = (it / kSt) & 1;
+          if (*abort_flag || !ptx::mbar_wait(full_b(s), par, a.err) || !ptx::mbar_wait(full_a(s), par, a.err)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t at = tmem + acol0 + kXtACols * s;
+          const uint64_t bd = ptx::smem_desc_sw128(b_tile(s));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
+            ptx::umma_f16_ts(acc, at + 8u * kk, bd + 2u * kk, idesc, (kb | kk) != 0);
+          ptx::umma_commit(empty(s));
+          issued = it + 1;
+        }
+        if (ok) ptx::umma_commit(acc_full(b));
+      }
+      if (!ok) *abort_flag = 1;
+      // The last commit covers every MMA before it: wait for it, so that TMEM and shared memory
+      // are not released under one (on a whole run the decode warps have waited already).
+      if (issued) ptx::mbar_wait(empty((issued - 1) % kSt), ((issued - 1) / kSt) & 1, a.err);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ codebooks and index slices
+    if (lane == 0 && (kBook || kStaged || kLadder)) {
+      const bool block_scales = a.w.scale_group == 64;
+      bool ok = true;
+      int js = 0, books = 0, last_e = -1;
+      for (int u = ubeg; ok && u < uend; ++u) {
+        const XtTile t = tile_of(u);
+        const LayerArgs l = expert_layer(a, t.e);
+        if ((kBook || (kLadder && a.w.n8)) && (books == 0 || (!a.shared && t.e != last_e))) {
+          if (*abort_flag || (books > 0 && !ptx::mbar_wait(cb_empty, (books - 1) & 1, a.err))) {
+            ok = false;
+            break;
+          }
+          if (kBook) {
+            ptx::mbar_arrive_expect_tx(cb_full, 65536u);
+            ptx::bulk_load(base, l.cb1, 65536u, cb_full);
+          } else {
+            ptx::mbar_arrive_expect_tx(cb_full, 4096u);
+            ptx::bulk_load(base, l.cb8, 4096u, cb_full);
+          }
+          ++books;
+        }
+        last_e = t.e;
+        if (!kStaged) continue;
+        // rows of W: one run of the tile's rows, or a gate run and an up run (64 rows apart in the slot)
+        const int r0 = out_tile * t.rt, nr = min(out_tile, a.Nout - r0), runs = a.glu ? 2 : 1;
+        for (int j = 0; j < nsl; ++j, ++js) {
+          const int sl = js % kXtSlots;
+          if (*abort_flag || (js >= kXtSlots && !ptx::mbar_wait(idx_empty(sl), ((js / kXtSlots) - 1) & 1, a.err))) {
+            ok = false;
+            break;
+          }
+          const int w = slice_width(j, G);
+          const uint32_t dst = base + kXtOffIdx + kXtIdxSlot * sl, bar = idx_full(sl);
+          const uint32_t per_row = (FMT == kFmtVq16 ? 2 * w : w + w / 2 * (kTwo ? 2 : 1)) + (block_scales ? w / 4 : 0);
+          ptx::mbar_arrive_expect_tx(bar, (uint32_t)(runs * nr) * per_row);
+          for (int h = 0; h < runs; ++h) {
+            const int64_t e = (int64_t)16 * j * N + (int64_t)(r0 + h * a.Nout) * w;  // entry of (slice j, first row)
+            const uint32_t o = 64u * h;                                             // first row in the slot
+            if (FMT == kFmtVq16) {
+              ptx::bulk_load(dst + o * w * 2, l.idx16 + e, nr * w * 2, bar);
+            } else {
+              ptx::bulk_load(dst + o * w, l.lo + e, nr * w, bar);
+              ptx::bulk_load(dst + kXtIdxHi + o * w / 2, l.hi4 + e / 2, nr * w / 2, bar);
+              if (kTwo) ptx::bulk_load(dst + kXtIdxS2 + o * w / 2, l.s2 + e / 2, nr * w / 2, bar);
+            }
+            if (block_scales) ptx::bulk_load(dst + kXtIdxSc + o * w / 4, l.scales + e / 8, nr * w / 4, bar);
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      for (int i = js > kXtSlots ? js - kXtSlots : 0; i < js; ++i)
+        ptx::mbar_wait(idx_full(i % kXtSlots), (i / kXtSlots) & 1, a.err);
+      if (books) ptx::mbar_wait(cb_full, (books - 1) & 1, a.err);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ decode
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const bool block_scales = a.w.scale_group == 64;
+    // Row of the tile in the index slot, and of the output: with glu lanes 0..15 of a quarter hold
+    // gate rows and lanes 16..31 the up rows of the same columns.
+    const int col = a.glu ? 16 * q + (lane & 15) : 32 * q + lane;  // column of y within the tile
+    const bool is_up = a.glu && lane >= 16;
+    const int srow = is_up ? 64 + col : col;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
+    bool ok = true;
+    int it0 = 0, js0 = 0, ui = 0, books = 0, last_e = -1;
+    uint32_t cb2r[4] = {0, 0, 0, 0};
+    for (int u = ubeg; ok && u < uend; ++u, ++ui) {
+      const XtTile t = tile_of(u);
+      const LayerArgs l = expert_layer(a, t.e);
+      const int n = out_tile * t.rt + col;  // column of y
+      const bool valid = n < a.Nout;
+      const int r = is_up ? a.Nout + n : n;  // row of W
+      if (books == 0 || (!a.shared && t.e != last_e)) {
+        if (kTwo) {
+          const uint4 v = reinterpret_cast<const uint4*>(l.cb2)[lane & 15];
+          cb2r[0] = v.x; cb2r[1] = v.y; cb2r[2] = v.z; cb2r[3] = v.w;
+        }
+        if (kBook || (kLadder && a.w.n8)) {
+          if (books > 0) {  // done with the codebook before
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(cb_empty);
+          }
+          if (*abort_flag || !ptx::mbar_wait(cb_full, books & 1, a.err)) ok = false;
+        }
+        ++books;
+      }
+      last_e = t.e;
+      const unsigned short row_scale = (!block_scales && valid) ? l.scales[r] : (unsigned short)0;
+      // this warp's blocks of the tile: those with (it0 + kb) % P == part
+      for (int kb = (part + kXtParts - it0 % kXtParts) % kXtParts; ok && kb < nkb; kb += kXtParts) {
+        const int it = it0 + kb, j = kb >> 1, h = kb & 1, js = js0 + j;
+        const int w = slice_width(j, G), st = it % kSt, sl = js % kXtSlots;
+        const uint32_t ta = tlane + acol0 + kXtACols * (uint32_t)st;
+        if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty(st), ((it / kSt) - 1) & 1, a.err)) ||
+            (kStaged && !ptx::mbar_wait(idx_full(sl), (js / kXtSlots) & 1, a.err))) {
+          ok = false;
+          break;
+        }
+        uint2 lo8 = make_uint2(0, 0);
+        uint32_t hi4w = 0, s24w = 0;
+        uint4 v16 = make_uint4(0, 0, 0, 0);
+        LadderIdx res{};
+        unsigned short sc = row_scale;
+        if (valid) {
+          if (kStaged) {
+            const unsigned char* slot = sm + kXtOffIdx + kXtIdxSlot * sl;
+            if (FMT == kFmtVq16) {
+              v16 = *reinterpret_cast<const uint4*>(slot + (srow * w + 8 * h) * 2);
+            } else {
+              lo8 = *reinterpret_cast<const uint2*>(slot + srow * w + 8 * h);
+              hi4w = *reinterpret_cast<const uint32_t*>(slot + kXtIdxHi + srow * (w / 2) + 4 * h);
+              if (kTwo) s24w = *reinterpret_cast<const uint32_t*>(slot + kXtIdxS2 + srow * (w / 2) + 4 * h);
+            }
+            if (block_scales) sc = *reinterpret_cast<const uint16_t*>(slot + kXtIdxSc + (srow * (w / 8) + h) * 2);
+          } else {
+            const int64_t e = (int64_t)16 * j * N + (int64_t)r * w + 8 * h;
+            if constexpr (kLadder) load_ladder_block(l, e, res);
+            v16 = *reinterpret_cast<const uint4*>(l.idx16 + e);
+            if (block_scales) sc = l.scales[scale_index(r, 128 * j + 64 * h, N, K, 64)];
+          }
+        }
+        if (kStaged) {
+          __syncwarp();
+          // a slice of one block is given back twice by its only decoder
+          if (lane == 0) {
+            ptx::mbar_arrive(idx_empty(sl));
+            if (w == 8) ptx::mbar_arrive(idx_empty(sl));
+          }
+        }
+        const float scf = kLadder ? __half2float(__ushort_as_half(sc)) : 0.f;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // 4 groups (16 TMEM columns) at a time
+          uint32_t out[16];
+          const uint32_t low = c ? lo8.y : lo8.x;
+          const uint32_t v0 = k16 ? (c ? v16.z : v16.x) : 0u, v1 = k16 ? (c ? v16.w : v16.y) : 0u;
+#pragma unroll
+          for (int g4 = 0; g4 < 4; ++g4) {
+            const int g = 4 * c + g4;
+            uint32_t i1;
+            if (k16)
+              i1 = ((g4 < 2 ? v0 : v1) >> (16 * (g4 & 1))) & 0xFFFFu;
+            else
+              i1 = ((low >> (8 * g4)) & 0xFFu) | (((hi4w >> (4 * g)) & 15u) << 8);
+            const uint4 c1 = kBook ? cb1s[i1] : __ldg(reinterpret_cast<const uint4*>(l.cb1) + i1);
+            if constexpr (kLadder) {
+              float v[8];
+              ladder_sum(l, res, g, c1, cb1s, v);
+              pack_scaled<T>(v, scf, out + 4 * g4);
+            } else {
+              uint32_t c2[4] = {0, 0, 0, 0};
+              if (kTwo) {
+                const int i2 = (int)((s24w >> (4 * g)) & 15u);
+#pragma unroll
+                for (int w4 = 0; w4 < 4; ++w4) c2[w4] = __shfl_sync(0xffffffffu, cb2r[w4], i2);
+              }
+              decode_scaled<T, kTwo>(c1, c2, sc, out + 4 * g4);
+            }
+          }
+          ptx::tmem_st16(ta + 16u * c, out);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full_a(st));
+      }
+      it0 += nkb;
+      js0 += nsl;
+
+      // ---------------------------------------------------------- epilogue
+      const int b = ui % nacc;
+      if (ok && (*abort_flag || !ptx::mbar_wait(acc_full(b), (ui / nacc) & 1, a.err))) ok = false;
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const float bv = (a.bias && valid) ? Elt<T>::to_f32(a.bias[(int64_t)t.e * N + r]) : 0.f;
+      for (int c0 = 16 * part; c0 < t.n; c0 += 16 * kXtParts) {
+        uint32_t v[16];
+        ptx::tmem_ld16(tlane + acols * b + c0, v);
+        ptx::tmem_wait_ld();
+        const int left = t.n - c0;
+        // rows of x that are out of range count as zeros
+        uint32_t bad = 0;
+        if (a.rows) {
+          const int xr = (lane < 16 && lane < left) ? a.rows[t.first + c0 + lane] : 0;
+          bad = __ballot_sync(0xffffffffu, xr < 0 || xr >= a.x_rows);
+        }
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = ((bad >> i) & 1u ? 0.f : __uint_as_float(v[i])) + bv;
+        uint16_t* y = a.y + (int64_t)(t.first + c0) * a.Nout + n;
+        if (!a.glu) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (valid && i < left) y[(int64_t)i * a.Nout] = Elt<T>::from_f32(apply_act(a.act, f[i]));
+        } else {
+          // gate lanes finish the even token of each pair, up lanes the odd one
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, is_up ? f[i] : f[i + 1], 16);
+            const float gate = is_up ? other : f[i], up = is_up ? f[i + 1] : other;
+            const int tok = is_up ? i + 1 : i;
+            if (valid && tok < left) y[(int64_t)tok * a.Nout] = Elt<T>::from_f32(gated(a.act, gate, up));
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(acc_empty(b));
+    }
+    if (!ok) *abort_flag = 1;
+  }
+
+  // Every thread of the block gets here (all waits above are bounded).
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, tcols);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFn>(ptr);
+    return static_cast<EncodeTiledFn>(nullptr);
+  }();
+  return fn;
+}
+
+template <int FMT, typename T, bool kStaged>
+static cudaError_t launch_xt_t(const ExpertsArgs& a, int Tmax, int num_sms, cudaStream_t s) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap map;
+  const CUtensorMapDataType dt =
+      a.w.act == VQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.w.K, (cuuint64_t)a.x_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.w.K * 2};
+  const cuuint32_t box[2] = {64, 1};  // gather4: one row high
+  const cuuint32_t estr[2] = {1, 1};
+  if (enc(&map, dt, 2, const_cast<uint16_t*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  auto kern = experts_tc_kernel<FMT, T, kStaged>;
+  const int smem = (int)xt_smem(Tmax);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int nacc = 2 * ((Tmax + 31) / 32 * 32) + kXtStages * (int)kXtACols <= 512 ? 2 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms);
+  cfg.blockDim = dim3(kXtThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, map, a, Tmax, nacc);
+}
+
+template <typename T>
+static cudaError_t launch_xt(const ExpertsArgs& a, int Tmax, int num_sms, cudaStream_t s) {
+  switch (a.w.fmt) {
+    case kFmtRvq12: return launch_xt_t<kFmtRvq12, T, true>(a, Tmax, num_sms, s);
+    case kFmtRvq12_4: return launch_xt_t<kFmtRvq12_4, T, true>(a, Tmax, num_sms, s);
+    case kFmtVq16Rvq: return launch_xt_t<kFmtVq16Rvq, T, false>(a, Tmax, num_sms, s);
+    default: return launch_xt_t<kFmtVq16, T, true>(a, Tmax, num_sms, s);
+  }
+}
+
+cudaError_t launch_experts_tc(const ExpertsArgs& a, int Tmax, int num_sms, cudaStream_t s) {
+  return a.w.act == VQ_BF16 ? launch_xt<__nv_bfloat16>(a, Tmax, num_sms, s) : launch_xt<__half>(a, Tmax, num_sms, s);
+}
+
+}  // namespace vq

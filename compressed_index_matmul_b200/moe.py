@@ -1,5 +1,5 @@
-"""Mixture-of-experts operators on compressed weights: the routing of tokens to experts and
-the weighted sum of the experts' rows back to the tokens."""
+"""Mixture-of-experts operators on compressed weights: the products grouped by expert, the
+routing of tokens to experts and the weighted sum of the experts' rows back to the tokens."""
 
 from __future__ import annotations
 
@@ -17,6 +17,124 @@ def _cuda_device(device) -> torch.device:
 
     device = torch.device(device)
     return torch.device("cuda", torch.cuda.current_device()) if device.type == "cuda" and device.index is None else device
+
+
+def _on_device(a, device):
+    """A plane, codebook or scale array on the device, its bits as they are."""
+    import numpy as np
+    import torch
+
+    if isinstance(a, np.ndarray):
+        a = np.ascontiguousarray(a)
+        a = torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a)
+    return a.to(device).contiguous()
+
+
+class VQExperts:
+    """E compressed weight matrices of one shape, multiplied group by group (vq_experts_forward).
+
+    ``arrays``: numpy arrays or torch tensors named as in ``VQLinear`` (lo, hi4, s2, idx16, idx8,
+    cb1, cb2, cbr, cb8, scales, mult), each with a leading dimension E in include/vqlinear.h's
+    storage format; the codebooks' is 1 (or left out) with `shared_codebooks`.  For the residual
+    ladder cbr is [n16 - 1, E or 1, 65536, 8] and idx16 [E, n16 * N * K / 8].
+    `glu`: rows [0, N/2) of every matrix are a gate, the others its up projection, and the output
+    has N/2 columns, act(gate) * up.  `act` is a VQ_ACT_*, `bias` [E, N] or None.
+    A call takes at most `max_rows` rows, all experts together."""
+
+    def __init__(self, E, N, K, fmt, scale_group, act_dtype, max_rows, arrays: dict, act=B.VQ_ACT_NONE, glu=False,
+                 bias=None, shared_codebooks=False, device="cuda"):
+        import numpy as np
+        import torch
+
+        self.handle = None
+        self.E, self.N, self.K, self.fmt, self.scale_group, self.act_dtype = E, N, K, fmt, scale_group, act_dtype
+        self.max_rows, self.act, self.glu, self.shared = max_rows, act, bool(glu), bool(shared_codebooks)
+        self.n_out = N // 2 if glu else N
+        self.device = dev = _cuda_device(device)
+        names = ("lo", "hi4", "s2", "idx16", "idx8", "cb1", "cb2", "cbr", "cb8", "scales")
+        t = self.t = {k: _on_device(arrays[k], dev) for k in names if arrays.get(k) is not None}
+        n, sets = N * (K // 8), 1 if shared_codebooks else E
+        ladder, k16 = fmt == B.VQ_FMT_VQ16_RVQ, fmt in (B.VQ_FMT_VQ16, B.VQ_FMT_VQ16_RVQ)
+        self.n16 = t["idx16"].numel() // (E * n) if ladder and "idx16" in t else 0
+        self.n8 = int(ladder and "idx8" in t)
+        self.mult = tuple(float(m) for m in np.asarray(arrays["mult"], dtype=np.float32)) if ladder else ()
+        want = {"scales": (E * N * (1 if scale_group == K else K // 64), 2), "cb1": (sets * (65536 if k16 else 4096) * 8, 2)}
+        if k16:
+            want["idx16"] = (E * n * max(1, self.n16), 2)
+        else:
+            want |= {"lo": (E * n, 1), "hi4": (E * n // 2, 1)}
+        if fmt == B.VQ_FMT_RVQ12_4:
+            want |= {"s2": (E * n // 2, 1), "cb2": (sets * 16 * 8, 2)}
+        if ladder and self.n16 > 1:
+            want["cbr"] = ((self.n16 - 1) * sets * 65536 * 8, 2)
+        if self.n8:
+            want |= {"idx8": (E * n, 1), "cb8": (sets * 256 * 8, 2)}
+        for name, (count, size) in want.items():
+            if name not in t or t[name].numel() != count or t[name].element_size() != size:
+                raise ValueError(f"{name} must have {count} entries of {size} bytes for E={E}, N={N}, K={K}: got "
+                                 f"{t[name].numel() if name in t else 'none'}")
+        self.bias = None
+        if bias is not None:
+            self.bias = bias.to(dev)
+            check_tensor(self.bias, "bias", (E, N), self.torch_dtype, dev)
+        cbr = tuple(t["cbr"].data_ptr() + i * sets * 65536 * 16 for i in range(self.n16 - 1)) if "cbr" in want else ()
+        self.planes = B.make_planes(t.get("lo"), t.get("hi4"), t.get("s2"), t.get("idx16"), t.get("idx8"))
+        self.codebooks = B.make_codebooks(t["cb1"], t.get("cb2"), cbr, t.get("cb8"))
+        with torch.cuda.device(dev):
+            self.handle = B.vq_experts_create(E, N, K, fmt, scale_group, act_dtype, max_rows, act, glu, shared_codebooks,
+                                              self.n16, self.n8, self.mult)
+
+    @property
+    def torch_dtype(self):
+        import torch
+
+        return torch.bfloat16 if self.act_dtype == B.VQ_BF16 else torch.float16
+
+    def forward(self, x, offsets, rows=None, y=None, stream=None):
+        """y[r] = act(x[rows[r]] . W_e^T + bias[e]) for offsets[e] <= r < offsets[e + 1].
+
+        x [x_rows, K]; offsets int32 [E + 1] and rows int32 [T] on the device, as ``VQRouter``
+        gives them; without `rows` row r reads x[r].  A `rows` value outside x reads as zeros.
+        Returns y [T, N] (glu: [T, N/2]); rows of y outside offsets[0] .. offsets[E] are not
+        written."""
+        import torch
+
+        dt, dev = self.torch_dtype, self.device
+        n = x.shape[0]
+        check_tensor(x, "x", (n, self.K), dt, dev)
+        check_tensor(offsets, "offsets", (self.E + 1,), torch.int32, dev)
+        T = n
+        if rows is not None:
+            T = rows.shape[0]
+            check_tensor(rows, "rows", (T,), torch.int32, dev)
+        if y is None:
+            y = torch.empty((T, self.n_out), dtype=dt, device=dev)
+        else:
+            check_tensor(y, "y", (T, self.n_out), dt, dev)
+        if T > 0:
+            B.vq_experts_forward(self.handle, x, n, rows, offsets, self.planes, self.codebooks, self.t["scales"], self.bias,
+                                 y, T, _raw_stream(stream, dev.index))
+        return y
+
+    __call__ = forward
+
+    def set_path(self, path: int):
+        """VQ_PATH_GEMV, VQ_PATH_TC or VQ_PATH_AUTO (vq_experts_set_path)."""
+        B.vq_experts_set_path(self.handle, path)
+
+    def plan(self, T: int) -> dict:
+        return B.vq_experts_plan(self.handle, T)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            B.vq_experts_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class VQRouting(NamedTuple):

@@ -1,10 +1,15 @@
 /*
  * vqlinear_ffn.h -- the feed-forward block around a codebook-VQ linear layer: a forward
- * with bias, activation, gate and residual in its epilogue.
+ * with bias, activation, gate and residual in its epilogue; the same product grouped by
+ * expert over ragged row counts; and the routing that feeds it (top-k experts of every
+ * token, the rows in expert order, and their weighted sum back to the tokens).
  *
  * The storage format, the element types and the conventions shared by every entry point
  * (status codes and vq_last_error, streams, ownership, 16-byte alignment of device
- * pointers, one call at a time per handle) are those stated in vqlinear.h.
+ * pointers, one call at a time per handle) are those stated in vqlinear.h.  Row counts
+ * per expert, row orders and routing results live on the device and are never read by
+ * the host, so every call here can be captured into a CUDA graph and replayed on other
+ * contents.
  */
 #ifndef VQLINEAR_FFN_H
 #define VQLINEAR_FFN_H
@@ -49,6 +54,67 @@ typedef struct {
 vq_status vq_linear_forward_epilogue(vq_linear_t h, const void* x, const int8_t* signs, const vq_planes* planes,
                                      const vq_codebooks* codebooks, const void* scales, const vq_epilogue* epi,
                                      void* y, int32_t M, int32_t N, int32_t K, void* stream);
+
+/* ---------------------------------------------------------- products grouped by expert */
+
+/* E weight matrices of one shape.  Expert e's planes, scales and (unless shared)
+ * codebooks follow expert e-1's without padding: planes->lo is [E][N*G] and so on, each
+ * in the storage format of a single layer (VQ_FMT_VQ16_RVQ: idx16 is [E][n16][N*G]);
+ * cb1 is [E][entries][8], and so are cb2, cbr[t] and cb8. */
+typedef struct {
+  vq_linear_desc layer;     /* N, K, fmt, scale_group, act_dtype, n16, n8, mult of every expert; max_M: the
+                               largest row count T of a call, all experts together; rht and corr must be 0
+                               (rotate x with vq_rht_apply).  N % 8 == 0 (N % 16 == 0 with glu), else
+                               VQ_ERR_UNSUPPORTED */
+  int32_t E;                /* 1 .. 1024 */
+  int32_t shared_codebooks; /* 1: one set of codebooks for all experts */
+  int32_t glu;              /* 1: rows [0, N/2) of W are a gate, rows [N/2, N) its up projection; y has N/2 columns */
+  int32_t act;              /* VQ_ACT_* */
+} vq_experts_desc;
+
+typedef struct vq_experts_s* vq_experts_t;
+
+/* Create a handle on the current device (allocates an error word; the kernels need no
+ * scratch).  Synchronous.  On error *out is set to NULL. */
+vq_status vq_experts_create(const vq_experts_desc* desc, vq_experts_t* out);
+
+/* As vq_linear_destroy. */
+vq_status vq_experts_destroy(vq_experts_t h);
+
+/* The rows r of expert e are offsets[e] <= r < offsets[e+1], and for each of them
+ *   y[r] = RN(act(x[rows[r]] . W_e^T + bias[e]))                              (glu == 0)
+ *   y[r] = RN(act(x[rows[r]] . G_e^T + bias[e][:N/2]) * (x[rows[r]] . U_e^T + bias[e][N/2:]))
+ * with G_e, U_e the first and second N/2 rows of W_e.
+ *   x        [x_rows][K], act_dtype
+ *   rows     device int32 [T], the x row of every row, or NULL: row r reads x[r] (x_rows
+ *            must then be at least T).  A value outside [0, x_rows) reads as a row of zeros.
+ *   offsets  device int32 [E+1], non-decreasing, offsets[0] >= 0, offsets[E] <= T; an
+ *            expert with offsets[e] == offsets[e+1] has no rows and its weights are not
+ *            read.  Values are clamped into [0, T] and to at least the ones before them, so
+ *            bad offsets give wrong rows but no access out of range.
+ *   bias     [E][N], act_dtype, or NULL
+ *   y        [T][N] (glu: [T][N/2]), act_dtype.  Rows below offsets[0] or from offsets[E]
+ *            on are left as they were.  y must not overlap any input.
+ * Accumulation is fp32.  The weights are rounded to act_dtype before the product, as
+ * the single-layer paths that materialise weights do (the scaled stage sum with one fused
+ * multiply-add per stage in fp32).  For a given kernel (below) the result of a row does not
+ * depend on the other rows, and is bit-identical from run to run.
+ * Enqueues one kernel on `stream`; nothing for T == 0. */
+vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_rows, const int32_t* rows,
+                             const int32_t* offsets, const vq_planes* planes, const vq_codebooks* codebooks,
+                             const void* scales, const void* bias, void* y, int32_t T, void* stream);
+
+/* The kernel of later forwards: VQ_PATH_GEMV (warp MMAs on weights decoded in registers;
+ * tiles of up to 16 rows of an expert), VQ_PATH_TC (tcgen05 on weights decoded into tensor
+ * memory; tiles of up to 256), or VQ_PATH_AUTO, which takes VQ_PATH_GEMV while T rows spread
+ * over min(E, T) experts come to at most 16 each (the counts themselves stay on the device). */
+vq_status vq_experts_set_path(vq_experts_t h, int32_t path);
+
+/* As vq_linear_plan, for a forward of T rows. */
+vq_status vq_experts_plan(vq_experts_t h, int32_t T, vq_plan_info* out);
+
+/* As vq_linear_check, for the waits of this handle's kernels. */
+vq_status vq_experts_check(vq_experts_t h, void* stream);
 
 /* ------------------------------------------------------------------------- routing */
 

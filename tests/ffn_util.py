@@ -56,3 +56,36 @@ def epilogue_bound(tol_f, f, act, dt, bias=None, mul=None, res=None):
     y = np.abs(epilogue64(f, act, bias, mul, res))
     fp32 = 2.0 ** -24 * (LIPSCHITZ * m * (np.abs(f) + np.abs(b)) + units * a * m + a * m + r)
     return LIPSCHITZ * tol_f * m + fp32 + half_step(dt) * (y + LIPSCHITZ * tol_f * m) + (2.0 ** -25 if dt == 0 else 0.0)
+
+
+def product_bound(x, w, dt):
+    """Bound on the error of x . w^T whose weights are rounded to the type and summed in fp32
+    (x [m, K], w [n, K] in 64 bits).  The weights' roundings are independent, zero on average and at
+    most half a step each, so their sum is within 7 u sqrt(sum x^2 w^2) except with probability
+    2 exp(-49 / 2) = 5e-11 per element (Hoeffding); fp16 weights below 2^-14 are rounded to
+    multiples of 2^-24.  The K additions and the decode's fp32 steps are each off by at most 2^-24 of
+    what they add up to."""
+    x2, w2, ax, aw = x * x, w * w, np.abs(x), np.abs(w)
+    tol = 7 * half_step(dt) * np.sqrt(x2 @ w2.T) + (x.shape[1] + 4) * 2.0 ** -24 * (ax @ aw.T)
+    if dt == 0:
+        tol = tol + 7 * 2.0 ** -25 * np.sqrt(x2.sum(1, keepdims=True))
+    return tol
+
+
+def glu64(f, act, bias=None):
+    f = f if bias is None else f + bias
+    h = f.shape[1] // 2
+    return act64(act, f[:, :h]) * f[:, h:]
+
+
+def glu_bound(tol_f, f, act, dt, bias=None):
+    """Bound on |y - glu64(f)|: the gate's error stretched by the activation times the up value,
+    and the up value's error times the gate's."""
+    h = f.shape[1] // 2
+    b = np.zeros(f.shape[1]) if bias is None else bias
+    gate, up = f[:, :h], f[:, h:] + b[h:]
+    tg = epilogue_bound(tol_f[:, :h], gate, act, 1, b[:h]) - half_step(1) * (np.abs(act64(act, gate + b[:h])) + LIPSCHITZ * tol_f[:, :h])
+    tu = tol_f[:, h:] + 2.0 ** -23 * (np.abs(f[:, h:]) + np.abs(b[h:]))
+    a = np.abs(act64(act, gate + b[:h]))
+    err = tg * (np.abs(up) + tu) + a * tu + 2.0 ** -23 * a * np.abs(up)
+    return err + half_step(dt) * (a * np.abs(up) + err) + (2.0 ** -25 if dt == 0 else 0.0)

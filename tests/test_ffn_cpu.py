@@ -44,7 +44,7 @@ def same_layout(tmp_path, names):
 
 
 def test_structs_match_the_header(tmp_path):
-    same_layout(tmp_path, ["vq_epilogue", "vq_router_desc"])
+    same_layout(tmp_path, ["vq_epilogue", "vq_experts_desc", "vq_router_desc"])
 
 
 def test_epilogue_rejects_a_null_handle(lib):
@@ -131,3 +131,29 @@ def test_combine_checks_its_tensors():
         vq.combine(torch.zeros(4, 8), None, None)
     with pytest.raises(ValueError, match="current CUDA device"):
         vq.combine(torch.zeros((4, 8), dtype=torch.float16), torch.zeros(2, 2), torch.zeros((2, 2), dtype=torch.int32))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(E=0), 1), (dict(E=1025), 2), (dict(glu=2), 1), (dict(act=5), 1), (dict(act=-1), 1), (dict(shared_codebooks=3), 1),
+    (dict(N=12), 2), (dict(N=72, glu=1), 2), (dict(K=72), 1), (dict(K=80), 2), (dict(fmt=9), 1), (dict(max_rows=0), 1),
+    (dict(rht=1), 2), (dict(corr=1), 2), (dict(N=1 << 24, max_rows=1 << 20, E=1024), 2),
+    (dict(fmt=B.VQ_FMT_VQ16_RVQ, n16=5), 1),
+])
+def test_experts_reject_bad_descriptors(lib, kw, status):
+    a = dict(E=4, N=64, K=128, fmt=B.VQ_FMT_RVQ12_4, scale_group=64, act_dtype=B.VQ_BF16, max_rows=16)
+    a.update(kw)
+    with pytest.raises(B.VQError) as ei:
+        B.vq_experts_create(**a)
+    assert ei.value.status == status
+
+
+def test_experts_null_arguments(lib):
+    h = ctypes.c_void_p(1)
+    assert lib.vq_experts_create(None, None) == B.VQ_ERR_INVALID_ARG
+    assert lib.vq_experts_create(None, ctypes.byref(h)) == B.VQ_ERR_INVALID_ARG and h.value is None
+    cb, pl = B.make_codebooks(16, 16), B.make_planes(16, 16, 16)
+    assert lib.vq_experts_forward(None, 16, 1, None, 16, pl, cb, 16, None, 16, 1, None) == B.VQ_ERR_INVALID_ARG
+    assert lib.vq_experts_set_path(None, 0) == B.VQ_ERR_INVALID_ARG
+    assert lib.vq_experts_plan(None, 1, None) == B.VQ_ERR_INVALID_ARG
+    assert lib.vq_experts_check(None, None) == B.VQ_ERR_INVALID_ARG
+    assert lib.vq_experts_destroy(None) == B.VQ_OK
