@@ -75,7 +75,7 @@ class vq_epilogue(ctypes.Structure):
 
 class vq_experts_desc(ctypes.Structure):
     _fields_ = [("layer", vq_linear_desc), ("E", ctypes.c_int32), ("shared_codebooks", ctypes.c_int32),
-                ("glu", ctypes.c_int32), ("act", ctypes.c_int32)]
+                ("glu", ctypes.c_int32), ("act", ctypes.c_int32), ("gather", ctypes.c_int32)]
 
 
 class vq_router_desc(ctypes.Structure):
@@ -285,9 +285,9 @@ def vq_linear_forward_epilogue(h, x, planes: vq_planes, codebooks: vq_codebooks,
 
 
 def vq_experts_create(E, N, K, fmt, scale_group, act_dtype, max_rows, act=VQ_ACT_NONE, glu=0, shared_codebooks=0, n16=0,
-                      n8=0, mult=(), rht=0, corr=0) -> int:
+                      n8=0, mult=(), gather=1, rht=0, corr=0) -> int:
     d = vq_experts_desc(make_desc(N, K, fmt, scale_group, act_dtype, max_rows, rht, n16, n8, mult, corr), E,
-                        int(shared_codebooks), int(glu), act)
+                        int(shared_codebooks), int(glu), act, int(gather))
     h = ctypes.c_void_p()
     _check(load().vq_experts_create(ctypes.byref(d), ctypes.byref(h)))
     return h.value

@@ -7,7 +7,7 @@
 
 namespace vq {
 cudaError_t launch_experts_gemv(const ExpertsArgs& a, int num_sms, cudaStream_t s);
-cudaError_t launch_experts_tc(const ExpertsArgs& a, int Tmax, int num_sms, cudaStream_t s);
+cudaError_t launch_experts_tc(const ExpertsArgs& a, void* xs, int Tmax, int num_sms, cudaStream_t s);
 }  // namespace vq
 
 using namespace vq;
@@ -17,6 +17,7 @@ struct vq_experts_s {
   DeviceInfo dev;
   int path;
   uint32_t* err;  // device word, set by bounded waits that gave up
+  void* xs;       // [max_M][K]: x in row order, for the tensor-core kernel (desc.gather == 1)
 };
 
 namespace {
@@ -46,6 +47,7 @@ vq_status validate_experts(const vq_experts_desc* d) {
   if (d->shared_codebooks != 0 && d->shared_codebooks != 1)
     return fail(VQ_ERR_INVALID_ARG, "shared_codebooks=%d must be 0 or 1", d->shared_codebooks);
   if (d->glu != 0 && d->glu != 1) return fail(VQ_ERR_INVALID_ARG, "glu=%d must be 0 or 1", d->glu);
+  if (d->gather != 0 && d->gather != 1) return fail(VQ_ERR_INVALID_ARG, "gather=%d must be 0 or 1", d->gather);
   if (d->act < VQ_ACT_NONE || d->act > VQ_ACT_GELU_TANH)
     return fail(VQ_ERR_INVALID_ARG, "act=%d is not a VQ_ACT_*", d->act);
   if (d->layer.rht || d->layer.corr)
@@ -74,13 +76,16 @@ VQ_API vq_status vq_experts_create(const vq_experts_desc* desc, vq_experts_t* ou
   h->dev = dev;
   h->path = VQ_PATH_AUTO;
   cudaError_t e = cudaMalloc(&h->err, sizeof(uint32_t));
+  const size_t xs_bytes = desc->gather ? (size_t)desc->layer.max_M * desc->layer.K * 2 : 0;
+  if (e == cudaSuccess && xs_bytes) e = cudaMalloc(&h->xs, xs_bytes);
   if (e == cudaSuccess) e = cudaMemset(h->err, 0, sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();  // the zeroing is complete before any forward
   if (e != cudaSuccess) {
     cudaFree(h->err);
+    cudaFree(h->xs);
     delete h;
     cudaGetLastError();
-    return fail(VQ_ERR_NOMEM, "cudaMalloc of the error word failed: %s", cudaGetErrorString(e));
+    return fail(VQ_ERR_NOMEM, "cudaMalloc of the error word and %zu bytes for x failed: %s", xs_bytes, cudaGetErrorString(e));
   }
   *out = h;
   return VQ_OK;
@@ -88,7 +93,7 @@ VQ_API vq_status vq_experts_create(const vq_experts_desc* desc, vq_experts_t* ou
 
 VQ_API vq_status vq_experts_destroy(vq_experts_t h) {
   if (h == nullptr) return VQ_OK;
-  cudaError_t e = free_on_device(h->dev.device, h->err);
+  cudaError_t e = free_on_device(h->dev.device, h->err, h->xs);
   delete h;
   return e == cudaSuccess ? VQ_OK : cuda_fail(e, "vq_experts_destroy");
 }
@@ -106,7 +111,7 @@ VQ_API vq_status vq_experts_plan(vq_experts_t h, int32_t T, vq_plan_info* out) {
   if (T < 1 || T > h->d.layer.max_M) return fail(VQ_ERR_INVALID_ARG, "T=%d outside [1, max_M=%d]", T, h->d.layer.max_M);
   const ExpertsPlan p = plan_experts(h->d, T, h->path);
   out->path = p.path;
-  out->launches = 1;
+  out->launches = p.path == VQ_PATH_TC && h->d.gather ? 2 : 1;
   out->ctas = h->dev.num_sms;
   out->splits = 1;
   return VQ_OK;
@@ -121,6 +126,7 @@ VQ_API vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_row
   if (T == 0) return VQ_OK;
   if (x_rows < 1 || (rows == nullptr && x_rows < T))
     return fail(VQ_ERR_INVALID_ARG, "x_rows=%d: need at least %d", x_rows, rows ? 1 : T);
+  if (rows && !h->d.gather) return fail(VQ_ERR_INVALID_ARG, "rows given, but the handle was created with gather = 0");
   vq_status st;
   if ((st = check_ptr(x, "x")) || (st = check_ptr(y, "y")) || (st = check_ptr(offsets, "offsets")) ||
       (st = validate_planes(d, planes)) || (st = validate_codebooks(d, codebooks, scales)))
@@ -150,7 +156,7 @@ VQ_API vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_row
   a.shared = h->d.shared_codebooks;
   const ExpertsPlan p = plan_experts(h->d, T, h->path);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = p.path == VQ_PATH_TC ? launch_experts_tc(a, p.Tmax, h->dev.num_sms, s)
+  cudaError_t e = p.path == VQ_PATH_TC ? launch_experts_tc(a, h->xs, p.Tmax, h->dev.num_sms, s)
                                        : launch_experts_gemv(a, h->dev.num_sms, s);
   return e == cudaSuccess ? VQ_OK : cuda_fail(e, "vq_experts_forward launch");
 }

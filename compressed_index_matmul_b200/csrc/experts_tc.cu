@@ -5,8 +5,8 @@
 // rows that go with them) x up to Tmax rows of x, over all of K.  The tiles of all experts are
 // numbered in expert order (find_tiles) and cut into one contiguous, equal range per block, so
 // a block changes its expert, and with it the codebook in shared memory, once or twice.
-//   warp 0     x: per 64-wide k block, gathers the tile's x rows (TMA tile::gather4, four rows
-//              a copy, 128-byte swizzle) into a ring of S stages
+//   warp 0     lane 0: x, per 64-wide k block, TMA loads of the tile's x rows (32 rows a copy,
+//              128-byte swizzle) into a ring of S stages
 //   warp 1     allocates TMEM; lane 0 issues tcgen05.mma (M = 128, N = the tile's rows rounded
 //              up to 16, K = 16), A from TMEM, B from shared memory, and commits each stage
 //   warp 2     lane 0: the expert's 12-bit codebook (one bulk copy when it changes) and, per
@@ -20,6 +20,10 @@
 // All rings run on across tiles: while the decode warps store one tile, x and the indices
 // of the next are already on their way.  With Tmax <= 192 the accumulator has two buffers, so
 // the MMAs of the next tile need not wait for the stores either.
+// Rows that come through `rows` are first copied into row order (gather_rows_kernel): T K
+// elements written and read once more, 15 us of the 300 us of a 16384 x 2048 gather into
+// 4096 x 2048 weights.  Gathering them in the x loads instead (TMA tile::gather4) took 40 ns per
+// four rows, 2.6 us a k block of 256 rows against the 0.5 us that its decode takes.
 // Every mbarrier wait is bounded; a timeout sets the handle's error word, and the block winds
 // down (waits for its own copies and MMAs, frees TMEM).
 #include <cuda.h>
@@ -46,13 +50,17 @@ constexpr uint32_t kXtOffX = (kXtOffIdx + kXtSlots * kXtIdxSlot + 1023) / 1024 *
 constexpr uint32_t xt_smem(int Tmax) { return kXtOffX + kXtStages * Tmax * 128u + 1024u; }
 static_assert(xt_smem(kXtMaxT) <= 232448, "shared memory of the widest tile");
 
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int c, int r0, int r1, int r2,
-                                            int r3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-      "%5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-      : "memory");
+constexpr int kXtBox = 32;  // x rows of one TMA load
+
+// xs[r] = x[rows[r]], zeros where the row is out of range.  One block per row.
+__global__ void __launch_bounds__(128) gather_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ rows,
+                                                          uint4* __restrict__ xs, int K8, int x_rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t r = blockIdx.x;
+  const int xr = rows[r];
+  const bool in = xr >= 0 && xr < x_rows;
+  for (int i = threadIdx.x; i < K8; i += 128) xs[r * K8 + i] = in ? x[(int64_t)xr * K8 + i] : make_uint4(0, 0, 0, 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // One tile: its expert, its place, its x rows.
@@ -154,39 +162,29 @@ __global__ void __launch_bounds__(kXtThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ x rows
-    int it = 0;
-    bool ok = true;
-    for (int u = ubeg; ok && u < uend; ++u) {
-      const XtTile t = tile_of(u);
-      // quads lane and lane + 32 of the tile's rows; places past the last row repeat it
-      int r[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int p = t.first + min(4 * (lane + 32 * h) + j, t.n - 1);
-          const int xr = a.rows ? a.rows[p] : p;
-          r[h][j] = (xr >= 0 && xr < a.x_rows) ? xr : 0;  // the epilogue replaces such a row by zeros
-        }
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int s = it % kSt;
-        if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty(s), ((it / kSt) - 1) & 1, a.err))) ok = false;
-        if (__any_sync(0xffffffffu, !ok)) {
-          *abort_flag = 1;
-          ok = false;
-          break;
-        }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)t.T * 128u);
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int qd = lane + 32 * h;
-          if (4 * qd < t.T) tma_gather4(b_tile(s) + 512u * qd, &xmap, 64 * kb, r[h][0], r[h][1], r[h][2], r[h][3], full_b(s));
+    if (lane == 0) {
+      ptx::prefetch_tensormap(&xmap);
+      int it = 0;
+      bool ok = true;
+      for (int u = ubeg; ok && u < uend; ++u) {
+        const XtTile t = tile_of(u);
+        const int boxes = (t.n + kXtBox - 1) / kXtBox;  // rows past the tile's are loaded and not used
+        for (int kb = 0; kb < nkb; ++kb) {
+          const int s = it % kSt;
+          if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty(s), ((it / kSt) - 1) & 1, a.err))) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)(boxes * kXtBox) * 128u);
+          for (int b = 0; b < boxes; ++b)
+            ptx::tma_load_2d(b_tile(s) + (uint32_t)(b * kXtBox) * 128u, &xmap, 64 * kb, t.first + kXtBox * b, full_b(s));
+          ++it;
         }
       }
+      // Do not leave while a copy into this block's shared memory may be in flight.
+      for (int i = it > kSt ? it - kSt : 0; i < it; ++i) ptx::mbar_wait(full_b(i % kSt), (i / kSt) & 1, a.err);
     }
-    // Do not leave while a copy into this block's shared memory may be in flight.
-    for (int i = it > kSt ? it - kSt : 0; i < it; ++i) ptx::mbar_wait(full_b(i % kSt), (i / kSt) & 1, a.err);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -410,15 +408,9 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         ptx::tmem_ld16(tlane + acols * b + c0, v);
         ptx::tmem_wait_ld();
         const int left = t.n - c0;
-        // rows of x that are out of range count as zeros
-        uint32_t bad = 0;
-        if (a.rows) {
-          const int xr = (lane < 16 && lane < left) ? a.rows[t.first + c0 + lane] : 0;
-          bad = __ballot_sync(0xffffffffu, xr < 0 || xr >= a.x_rows);
-        }
         float f[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = ((bad >> i) & 1u ? 0.f : __uint_as_float(v[i])) + bv;
+        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]) + bv;
         uint16_t* y = a.y + (int64_t)(t.first + c0) * a.Nout + n;
         if (!a.glu) {
 #pragma unroll
@@ -470,15 +462,32 @@ static EncodeTiledFn encode_fn() {
 }
 
 template <int FMT, typename T, bool kStaged>
-static cudaError_t launch_xt_t(const ExpertsArgs& a, int Tmax, int num_sms, cudaStream_t s) {
+static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, cudaStream_t s) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (a.rows) {  // x in row order
+    cfg.gridDim = dim3(a.T);
+    cfg.blockDim = dim3(128);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gather_rows_kernel, reinterpret_cast<const uint4*>(a.x), a.rows,
+                                       static_cast<uint4*>(xs), a.w.K / 8, a.x_rows);
+    if (e != cudaSuccess) return e;
+    a.x = static_cast<const uint16_t*>(xs);
+    a.rows = nullptr;
+    a.x_rows = a.T;
+  }
   CUtensorMap map;
   const CUtensorMapDataType dt =
       a.w.act == VQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t dims[2] = {(cuuint64_t)a.w.K, (cuuint64_t)a.x_rows};
   const cuuint64_t strides[1] = {(cuuint64_t)a.w.K * 2};
-  const cuuint32_t box[2] = {64, 1};  // gather4: one row high
+  const cuuint32_t box[2] = {64, kXtBox};
   const cuuint32_t estr[2] = {1, 1};
   if (enc(&map, dt, 2, const_cast<uint16_t*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -489,31 +498,24 @@ static cudaError_t launch_xt_t(const ExpertsArgs& a, int Tmax, int num_sms, cuda
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int nacc = 2 * ((Tmax + 31) / 32 * 32) + kXtStages * (int)kXtACols <= 512 ? 2 : 1;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms);
   cfg.blockDim = dim3(kXtThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, map, a, Tmax, nacc);
 }
 
 template <typename T>
-static cudaError_t launch_xt(const ExpertsArgs& a, int Tmax, int num_sms, cudaStream_t s) {
+static cudaError_t launch_xt(const ExpertsArgs& a, void* xs, int Tmax, int num_sms, cudaStream_t s) {
   switch (a.w.fmt) {
-    case kFmtRvq12: return launch_xt_t<kFmtRvq12, T, true>(a, Tmax, num_sms, s);
-    case kFmtRvq12_4: return launch_xt_t<kFmtRvq12_4, T, true>(a, Tmax, num_sms, s);
-    case kFmtVq16Rvq: return launch_xt_t<kFmtVq16Rvq, T, false>(a, Tmax, num_sms, s);
-    default: return launch_xt_t<kFmtVq16, T, true>(a, Tmax, num_sms, s);
+    case kFmtRvq12: return launch_xt_t<kFmtRvq12, T, true>(a, xs, Tmax, num_sms, s);
+    case kFmtRvq12_4: return launch_xt_t<kFmtRvq12_4, T, true>(a, xs, Tmax, num_sms, s);
+    case kFmtVq16Rvq: return launch_xt_t<kFmtVq16Rvq, T, false>(a, xs, Tmax, num_sms, s);
+    default: return launch_xt_t<kFmtVq16, T, true>(a, xs, Tmax, num_sms, s);
   }
 }
 
-cudaError_t launch_experts_tc(const ExpertsArgs& a, int Tmax, int num_sms, cudaStream_t s) {
-  return a.w.act == VQ_BF16 ? launch_xt<__nv_bfloat16>(a, Tmax, num_sms, s) : launch_xt<__half>(a, Tmax, num_sms, s);
+cudaError_t launch_experts_tc(const ExpertsArgs& a, void* xs, int Tmax, int num_sms, cudaStream_t s) {
+  return a.w.act == VQ_BF16 ? launch_xt<__nv_bfloat16>(a, xs, Tmax, num_sms, s) : launch_xt<__half>(a, xs, Tmax, num_sms, s);
 }
 
 }  // namespace vq

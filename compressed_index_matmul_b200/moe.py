@@ -39,10 +39,11 @@ class VQExperts:
     ladder cbr is [n16 - 1, E or 1, 65536, 8] and idx16 [E, n16 * N * K / 8].
     `glu`: rows [0, N/2) of every matrix are a gate, the others its up projection, and the output
     has N/2 columns, act(gate) * up.  `act` is a VQ_ACT_*, `bias` [E, N] or None.
-    A call takes at most `max_rows` rows, all experts together."""
+    A call takes at most `max_rows` rows, all experts together.  `gather`: calls may pass `rows`,
+    for which the handle keeps a buffer of max_rows x K elements."""
 
     def __init__(self, E, N, K, fmt, scale_group, act_dtype, max_rows, arrays: dict, act=B.VQ_ACT_NONE, glu=False,
-                 bias=None, shared_codebooks=False, device="cuda"):
+                 bias=None, shared_codebooks=False, gather=True, device="cuda"):
         import numpy as np
         import torch
 
@@ -82,7 +83,7 @@ class VQExperts:
         self.codebooks = B.make_codebooks(t["cb1"], t.get("cb2"), cbr, t.get("cb8"))
         with torch.cuda.device(dev):
             self.handle = B.vq_experts_create(E, N, K, fmt, scale_group, act_dtype, max_rows, act, glu, shared_codebooks,
-                                              self.n16, self.n8, self.mult)
+                                              self.n16, self.n8, self.mult, gather)
 
     @property
     def torch_dtype(self):

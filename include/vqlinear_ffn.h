@@ -70,12 +70,14 @@ typedef struct {
   int32_t shared_codebooks; /* 1: one set of codebooks for all experts */
   int32_t glu;              /* 1: rows [0, N/2) of W are a gate, rows [N/2, N) its up projection; y has N/2 columns */
   int32_t act;              /* VQ_ACT_* */
+  int32_t gather;           /* 1: calls may give `rows`; create then allocates max_M x K elements, where the
+                               tensor-core kernel's calls put x in row order */
 } vq_experts_desc;
 
 typedef struct vq_experts_s* vq_experts_t;
 
-/* Create a handle on the current device (allocates an error word; the kernels need no
- * scratch).  Synchronous.  On error *out is set to NULL. */
+/* Create a handle on the current device (allocates an error word and, with gather, the
+ * buffer for x).  Synchronous.  On error *out is set to NULL. */
 vq_status vq_experts_create(const vq_experts_desc* desc, vq_experts_t* out);
 
 /* As vq_linear_destroy. */
@@ -86,8 +88,8 @@ vq_status vq_experts_destroy(vq_experts_t h);
  *   y[r] = RN(act(x[rows[r]] . G_e^T + bias[e][:N/2]) * (x[rows[r]] . U_e^T + bias[e][N/2:]))
  * with G_e, U_e the first and second N/2 rows of W_e.
  *   x        [x_rows][K], act_dtype
- *   rows     device int32 [T], the x row of every row, or NULL: row r reads x[r] (x_rows
- *            must then be at least T).  A value outside [0, x_rows) reads as a row of zeros.
+ *   rows     device int32 [T], the x row of every row (desc.gather == 1), or NULL: row r reads
+ *            x[r] (x_rows must then be at least T).  A value outside [0, x_rows) reads as a row of zeros.
  *   offsets  device int32 [E+1], non-decreasing, offsets[0] >= 0, offsets[E] <= T; an
  *            expert with offsets[e] == offsets[e+1] has no rows and its weights are not
  *            read.  Values are clamped into [0, T] and to at least the ones before them, so
@@ -99,7 +101,7 @@ vq_status vq_experts_destroy(vq_experts_t h);
  * the single-layer paths that materialise weights do (the scaled stage sum with one fused
  * multiply-add per stage in fp32).  For a given kernel (below) the result of a row does not
  * depend on the other rows, and is bit-identical from run to run.
- * Enqueues one kernel on `stream`; nothing for T == 0. */
+ * Enqueues one kernel on `stream` (two where VQ_PATH_TC is given rows); nothing for T == 0. */
 vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_rows, const int32_t* rows,
                              const int32_t* offsets, const vq_planes* planes, const vq_codebooks* codebooks,
                              const void* scales, const void* bias, void* y, int32_t T, void* stream);
@@ -110,7 +112,7 @@ vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_rows, cons
  * over min(E, T) experts come to at most 16 each (the counts themselves stay on the device). */
 vq_status vq_experts_set_path(vq_experts_t h, int32_t path);
 
-/* As vq_linear_plan, for a forward of T rows. */
+/* As vq_linear_plan, for a forward of T rows (launches: with rows, if desc.gather == 1). */
 vq_status vq_experts_plan(vq_experts_t h, int32_t T, vq_plan_info* out);
 
 /* As vq_linear_check, for the waits of this handle's kernels. */

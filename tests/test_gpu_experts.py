@@ -405,6 +405,8 @@ def test_refusals():
         X.forward(flat[:T * K].view(T, K), off, y=flat[T * K // 2:T * K // 2 + T * N].view(T, N))
     with pytest.raises(vq.VQError, match="16-byte"):
         X.forward(flat[4:4 + T * K].view(T, K), off)
+    with pytest.raises(vq.VQError, match="gather"):
+        vq.VQExperts(E, N, K, FMT_RVQ12_4, 64, DT_BF16, T, arrays, gather=False).forward(x, off, rows=rows)
     with pytest.raises(vq.VQError, match="VQ_PATH"):
         X.set_path(vq.VQ_PATH_LUT)
     with pytest.raises(ValueError, match="must have"):
