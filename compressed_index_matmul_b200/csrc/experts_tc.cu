@@ -12,13 +12,13 @@
 //   warp 2     lane 0: the expert's 12-bit codebook (one bulk copy when it changes) and, per
 //              128-input slice, the tile's index bytes (one contiguous run per plane; glu: two)
 //              into a ring of slots
-//   warps 4..  decode: three per TMEM lane quarter; thread = one row of the tile (its lane).
-//              Block `it` of the block's whole sequence goes to warp it % 3 of every quarter, into A
-//              stage it % S.  After a tile's last block the same threads read the accumulator,
-//              apply bias and activation and store y: consecutive lanes are consecutive
-//              columns, and rows past the expert's last are not written.
+//   warps 4..  decode: four per TMEM lane quarter; thread = one row of the tile (its lane).
+//              Slice `js` of the block's whole sequence goes to warp js % 4 of every quarter, into A
+//              stage js % 4 (64 TMEM columns, 128 inputs).  After a tile's last slice the same
+//              threads read the accumulator, apply bias and activation and store y: consecutive
+//              lanes are consecutive columns, and rows past the expert's last are not written.
 // All rings run on across tiles: while the decode warps store one tile, x and the indices
-// of the next are already on their way.  With Tmax <= 192 the accumulator has two buffers, so
+// of the next are already on their way.  With Tmax <= 128 the accumulator has two buffers, so
 // the MMAs of the next tile need not wait for the stores either.
 // Rows that come through `rows` are first copied into row order (gather_rows_kernel): T K
 // elements written and read once more, 15 us of the 300 us of a 16384 x 2048 gather into
@@ -35,13 +35,13 @@
 namespace vq {
 
 constexpr int kXtRows = 128;
-constexpr int kXtParts = 3;                            // decode warps per TMEM lane quarter
+constexpr int kXtParts = 4;                            // decode warps per TMEM lane quarter, and A stages
 constexpr int kXtDecode = 4 * kXtParts;                // decode warps
 constexpr int kXtThreads = 32 * (4 + kXtDecode);
-constexpr int kXtStages = 4;
+constexpr int kXtStages = 4;                           // x stages of 64 inputs
 constexpr int kXtMaxT = 256;
-constexpr int kXtSlots = 4;                            // index slices in flight
-constexpr uint32_t kXtACols = 32;                      // TMEM columns of one A stage
+constexpr int kXtSlots = kXtParts;                     // index slices in flight
+constexpr uint32_t kXtACols = 64;                      // TMEM columns of one A stage (128 k of 16-bit pairs)
 constexpr uint32_t kXtIdxHi = 2048, kXtIdxS2 = 3072, kXtIdxSc = 4096, kXtIdxSlot = 4608;
 constexpr uint32_t kXtOffTiles = 65536;                // after the codebook
 constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 16;
@@ -78,7 +78,6 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   constexpr bool kBook = !k16;
   constexpr bool kTwo = (FMT == kFmtRvq12_4);
   static_assert(!(kLadder && kStaged), "the residual ladder reads its indices directly");
-  static_assert(kXtStages >= kXtParts, "a stage barrier may be at most one phase behind");
   constexpr int kSt = kXtStages;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // the swizzle of the x tiles goes by address bits
@@ -86,15 +85,16 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   const uint4* cb1s = reinterpret_cast<const uint4*>(sm);
   ExpertTiles& tiles = *reinterpret_cast<ExpertTiles*>(sm + kXtOffTiles);
   const uint32_t bar0 = base + kXtOffBars;
-  auto full_a = [&](int s) { return bar0 + 8u * s; };
-  auto full_b = [&](int s) { return bar0 + 8u * (kSt + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (2 * kSt + s); };
-  auto acc_full = [&](int b) { return bar0 + 8u * (3 * kSt + b); };
-  auto acc_empty = [&](int b) { return bar0 + 8u * (3 * kSt + 2 + b); };
-  const uint32_t cb_full = bar0 + 8u * (3 * kSt + 4), cb_empty = cb_full + 8u;
-  auto idx_full = [&](int s) { return cb_empty + 8u + 8u * s; };
-  auto idx_empty = [&](int s) { return cb_empty + 8u + 8u * (kXtSlots + s); };
-  static_assert(8 * (3 * kSt + 6 + 2 * kXtSlots) <= 256, "barriers overlap the flags");
+  auto full_b = [&](int s) { return bar0 + 8u * s; };
+  auto empty_b = [&](int s) { return bar0 + 8u * (kSt + s); };
+  auto acc_full = [&](int b) { return bar0 + 8u * (2 * kSt + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kSt + 2 + b); };
+  const uint32_t cb_full = bar0 + 8u * (2 * kSt + 4), cb_empty = cb_full + 8u, bar1 = cb_full + 16u;
+  auto full_a = [&](int s) { return bar1 + 8u * s; };
+  auto empty_a = [&](int s) { return bar1 + 8u * (kXtParts + s); };
+  auto idx_full = [&](int s) { return bar1 + 8u * (2 * kXtParts + s); };
+  auto idx_empty = [&](int s) { return bar1 + 8u * (3 * kXtParts + s); };
+  static_assert(8 * (2 * kSt + 6 + 4 * kXtParts) <= 256, "barriers overlap the flags");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kXtOffBars + 256);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kXtOffBars + 260);
   int* part_sums = reinterpret_cast<int*>(sm + kXtOffBars + 264);  // 2 per warp
@@ -109,14 +109,12 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   const int RT = (a.Nout + out_tile - 1) / out_tile;
   const uint32_t acols = ((uint32_t)Tmax + 31u) & ~31u;
   const uint32_t acol0 = acols * nacc;  // then the A stages
-  const uint32_t tneed = acol0 + kSt * kXtACols;
-  const uint32_t tcols = tneed <= 256 ? 256u : 512u;
+  const uint32_t tcols = 512u;  // acol0 + kXtParts * kXtACols is above 256
 
   if (tid == 0) {
     for (int s = 0; s < kSt; ++s) {
-      ptx::mbar_init(full_a(s), 4);  // one decode warp per TMEM lane quarter
-      ptx::mbar_init(full_b(s), 1);  // the x warp's expect_tx arrival (+ bytes)
-      ptx::mbar_init(empty(s), 1);   // one tcgen05.commit
+      ptx::mbar_init(full_b(s), 1);   // the x warp's expect_tx arrival (+ bytes)
+      ptx::mbar_init(empty_b(s), 1);  // one tcgen05.commit
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(acc_full(b), 1);
@@ -124,9 +122,11 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     }
     ptx::mbar_init(cb_full, 1);
     ptx::mbar_init(cb_empty, kXtDecode);
-    for (int s = 0; s < kXtSlots; ++s) {
+    for (int s = 0; s < kXtParts; ++s) {
+      ptx::mbar_init(full_a(s), 4);     // one decode warp per TMEM lane quarter
+      ptx::mbar_init(empty_a(s), 1);    // one tcgen05.commit
       ptx::mbar_init(idx_full(s), 1);
-      ptx::mbar_init(idx_empty(s), 8);  // the warps that decode the slice's two blocks
+      ptx::mbar_init(idx_empty(s), 4);  // the warps that decode the slice
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         const int boxes = (t.n + kXtBox - 1) / kXtBox;  // rows past the tile's are loaded and not used
         for (int kb = 0; kb < nkb; ++kb) {
           const int s = it % kSt;
-          if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty(s), ((it / kSt) - 1) & 1, a.err))) {
+          if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty_b(s), ((it / kSt) - 1) & 1, a.err))) {
             *abort_flag = 1;
             ok = false;
             break;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     if (lane == 0) {
       constexpr uint32_t kAbFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       bool ok = true;
-      int it = 0, ui = 0, issued = 0;
+      int it = 0, js = 0, ui = 0;
       for (int u = ubeg; ok && u < uend; ++u, ++ui) {
         const XtTile t = tile_of(u);
         const uint32_t idesc = ptx::idesc_f16(kAbFmt, kXtRows, (uint32_t)t.T);
@@ -202,28 +202,38 @@ __global__ void __launch_bounds__(kXtThreads, 1)
           break;
         }
         ptx::tc_fence_after();
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % kSt;
-          const uint32_t par = (it / kSt) & 1;
-          if (*abort_flag || !ptx::mbar_wait(full_b(s), par, a.err) || !ptx::mbar_wait(full_a(s), par, a.err)) {
+        for (int kb = 0; ok && kb < nkb; ++js) {
+          const int st = js % kXtParts;
+          if (*abort_flag || !ptx::mbar_wait(full_a(st), (js / kXtParts) & 1, a.err)) {
             ok = false;
             break;
           }
-          ptx::tc_fence_after();
-          const uint32_t at = tmem + acol0 + kXtACols * s;
-          const uint64_t bd = ptx::smem_desc_sw128(b_tile(s));
+          const uint32_t at = tmem + acol0 + kXtACols * st;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
-            ptx::umma_f16_ts(acc, at + 8u * kk, bd + 2u * kk, idesc, (kb | kk) != 0);
-          ptx::umma_commit(empty(s));
-          issued = it + 1;
+          for (int h = 0; h < 2; ++h) {  // the slice's blocks of 64 inputs
+            if (kb >= nkb) break;
+            const int s = it % kSt;
+            if (!ptx::mbar_wait(full_b(s), (it / kSt) & 1, a.err)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint64_t bd = ptx::smem_desc_sw128(b_tile(s));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
+              ptx::umma_f16_ts(acc, at + 32u * h + 8u * kk, bd + 2u * kk, idesc, (kb | kk) != 0);
+            ptx::umma_commit(empty_b(s));
+            ++it;
+            ++kb;
+          }
+          if (ok) ptx::umma_commit(empty_a(st));
         }
         if (ok) ptx::umma_commit(acc_full(b));
       }
       if (!ok) *abort_flag = 1;
       // The last commit covers every MMA before it: wait for it, so that TMEM and shared memory
       // are not released under one (on a whole run the decode warps have waited already).
-      if (issued) ptx::mbar_wait(empty((issued - 1) % kSt), ((issued - 1) / kSt) & 1, a.err);
+      if (it) ptx::mbar_wait(empty_b((it - 1) % kSt), ((it - 1) / kSt) & 1, a.err);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ codebooks and index slices
@@ -292,8 +302,57 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     const int srow = is_up ? 64 + col : col;
     const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
     bool ok = true;
-    int it0 = 0, js0 = 0, ui = 0, books = 0, last_e = -1;
+    int js0 = 0, ui = 0, books = 0, last_e = -1;
     uint32_t cb2r[4] = {0, 0, 0, 0};
+    XtTile prev{};         // the tile before, whose sums this warp has not stored yet
+    bool pending = false;
+
+    // Bias, activation and stores of tile `t`, the block's ui-th.  A warp does it after its first
+    // block of the next tile, so that the tensor cores finish the tile's last blocks meanwhile and
+    // find the next tile's first ones decoded.
+    auto finish_tile = [&](const XtTile& t, int ui) {
+      const int n = out_tile * t.rt + col;
+      const bool valid = n < a.Nout;
+      const int r = is_up ? a.Nout + n : n;
+      const int b = ui % nacc;
+      if (*abort_flag || !ptx::mbar_wait(acc_full(b), (ui / nacc) & 1, a.err)) return false;
+      ptx::tc_fence_after();
+      const float bv = (a.bias && valid) ? Elt<T>::to_f32(a.bias[(int64_t)t.e * N + r]) : 0.f;
+      for (int c0 = 16 * part; c0 < t.n; c0 += 16 * kXtParts) {
+        uint32_t v[16];
+        ptx::tmem_ld16(tlane + acols * b + c0, v);
+        ptx::tmem_wait_ld();
+        const int left = t.n - c0;
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]) + bv;
+        uint16_t* y = a.y + (int64_t)(t.first + c0) * a.Nout + n;
+        if (!a.glu) {
+          apply_act_all(a.act, f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (valid && i < left) y[(int64_t)i * a.Nout] = Elt<T>::from_f32(f[i]);
+        } else {
+          // gate lanes finish the even token of each pair, up lanes the odd one
+          float gate[8], up[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, is_up ? f[2 * i] : f[2 * i + 1], 16);
+            gate[i] = is_up ? other : f[2 * i];
+            up[i] = is_up ? f[2 * i + 1] : other;
+          }
+          apply_act_all(a.act, gate);
+          if (is_up) y += a.Nout;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (valid && 2 * i + (is_up ? 1 : 0) < left) y[(int64_t)(2 * i) * a.Nout] = Elt<T>::from_f32(gate[i] * up[i]);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(acc_empty(b));
+      return true;
+    };
     for (int u = ubeg; ok && u < uend; ++u, ++ui) {
       const XtTile t = tile_of(u);
       const LayerArgs l = expert_layer(a, t.e);
@@ -316,121 +375,127 @@ __global__ void __launch_bounds__(kXtThreads, 1)
       }
       last_e = t.e;
       const unsigned short row_scale = (!block_scales && valid) ? l.scales[r] : (unsigned short)0;
-      // this warp's blocks of the tile: those with (it0 + kb) % P == part
-      for (int kb = (part + kXtParts - it0 % kXtParts) % kXtParts; ok && kb < nkb; kb += kXtParts) {
-        const int it = it0 + kb, j = kb >> 1, h = kb & 1, js = js0 + j;
-        const int w = slice_width(j, G), st = it % kSt, sl = js % kXtSlots;
-        const uint32_t ta = tlane + acol0 + kXtACols * (uint32_t)st;
-        if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty(st), ((it / kSt) - 1) & 1, a.err)) ||
-            (kStaged && !ptx::mbar_wait(idx_full(sl), (js / kXtSlots) & 1, a.err))) {
+      // this warp's slices of the tile: those with (js0 + j) % P == part, all into its own A stage
+      const uint32_t ta = tlane + acol0 + kXtACols * (uint32_t)part;
+      for (int j = (part + kXtParts - js0 % kXtParts) % kXtParts; ok && j < nsl; j += kXtParts) {
+        const int w = slice_width(j, G), round = (js0 + j) / kXtParts;
+        if (*abort_flag || (kStaged && !ptx::mbar_wait(idx_full(part), round & 1, a.err))) {
           ok = false;
           break;
         }
-        uint2 lo8 = make_uint2(0, 0);
-        uint32_t hi4w = 0, s24w = 0;
-        uint4 v16 = make_uint4(0, 0, 0, 0);
-        LadderIdx res{};
-        unsigned short sc = row_scale;
+        uint32_t lo[k16 ? 8 : 4], hi[2] = {0, 0}, s2[2] = {0, 0}, sc2 = row_scale * 0x10001u;
+#pragma unroll
+        for (int i = 0; i < (k16 ? 8 : 4); ++i) lo[i] = 0;
         if (valid) {
           if (kStaged) {
-            const unsigned char* slot = sm + kXtOffIdx + kXtIdxSlot * sl;
-            if (FMT == kFmtVq16) {
-              v16 = *reinterpret_cast<const uint4*>(slot + (srow * w + 8 * h) * 2);
-            } else {
-              lo8 = *reinterpret_cast<const uint2*>(slot + srow * w + 8 * h);
-              hi4w = *reinterpret_cast<const uint32_t*>(slot + kXtIdxHi + srow * (w / 2) + 4 * h);
-              if (kTwo) s24w = *reinterpret_cast<const uint32_t*>(slot + kXtIdxS2 + srow * (w / 2) + 4 * h);
+            const unsigned char* slot = sm + kXtOffIdx + kXtIdxSlot * part;
+            if (w == 16) {
+              const uint4 v = *reinterpret_cast<const uint4*>(slot + srow * (k16 ? 32 : 16));
+              lo[0] = v.x; lo[1] = v.y; lo[2] = v.z; lo[3] = v.w;
+              if constexpr (k16) {
+                const uint4 v2 = *reinterpret_cast<const uint4*>(slot + srow * 32 + 16);
+                lo[4] = v2.x; lo[5] = v2.y; lo[6] = v2.z; lo[7] = v2.w;
+              } else {
+                const uint2 h = *reinterpret_cast<const uint2*>(slot + kXtIdxHi + srow * 8);
+                hi[0] = h.x; hi[1] = h.y;
+                if (kTwo) {
+                  const uint2 q2 = *reinterpret_cast<const uint2*>(slot + kXtIdxS2 + srow * 8);
+                  s2[0] = q2.x; s2[1] = q2.y;
+                }
+              }
+              if (block_scales) sc2 = *reinterpret_cast<const uint32_t*>(slot + kXtIdxSc + srow * 4);
+            } else {  // a 64-wide last slice
+              if constexpr (k16) {
+                const uint4 v = *reinterpret_cast<const uint4*>(slot + srow * 16);
+                lo[0] = v.x; lo[1] = v.y; lo[2] = v.z; lo[3] = v.w;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(slot + srow * 8);
+                lo[0] = v.x; lo[1] = v.y;
+                hi[0] = *reinterpret_cast<const uint32_t*>(slot + kXtIdxHi + srow * 4);
+                if (kTwo) s2[0] = *reinterpret_cast<const uint32_t*>(slot + kXtIdxS2 + srow * 4);
+              }
+              if (block_scales) sc2 = *reinterpret_cast<const uint16_t*>(slot + kXtIdxSc + srow * 2);
             }
-            if (block_scales) sc = *reinterpret_cast<const uint16_t*>(slot + kXtIdxSc + (srow * (w / 8) + h) * 2);
-          } else {
-            const int64_t e = (int64_t)16 * j * N + (int64_t)r * w + 8 * h;
-            if constexpr (kLadder) load_ladder_block(l, e, res);
-            v16 = *reinterpret_cast<const uint4*>(l.idx16 + e);
-            if (block_scales) sc = l.scales[scale_index(r, 128 * j + 64 * h, N, K, 64)];
+          } else if constexpr (k16) {
+            const int64_t e = (int64_t)16 * j * N + (int64_t)r * w;
+            const uint4 v = *reinterpret_cast<const uint4*>(l.idx16 + e);
+            lo[0] = v.x; lo[1] = v.y; lo[2] = v.z; lo[3] = v.w;
+            if (w == 16) {
+              const uint4 v2 = *reinterpret_cast<const uint4*>(l.idx16 + e + 8);
+              lo[4] = v2.x; lo[5] = v2.y; lo[6] = v2.z; lo[7] = v2.w;
+            }
+            if (block_scales)
+              sc2 = w == 16 ? *reinterpret_cast<const uint32_t*>(l.scales + e / 8) : (uint32_t)l.scales[e / 8];
           }
         }
         if (kStaged) {
           __syncwarp();
-          // a slice of one block is given back twice by its only decoder
-          if (lane == 0) {
-            ptx::mbar_arrive(idx_empty(sl));
-            if (w == 8) ptx::mbar_arrive(idx_empty(sl));
-          }
+          if (lane == 0) ptx::mbar_arrive(idx_empty(part));
         }
-        const float scf = kLadder ? __half2float(__ushort_as_half(sc)) : 0.f;
-        ptx::tc_fence_after();
+        bool waited = round == 0;  // the MMAs of this stage's slice before are done
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // 4 groups (16 TMEM columns) at a time
-          uint32_t out[16];
-          const uint32_t low = c ? lo8.y : lo8.x;
-          const uint32_t v0 = k16 ? (c ? v16.z : v16.x) : 0u, v1 = k16 ? (c ? v16.w : v16.y) : 0u;
+        for (int h = 0; h < 2; ++h) {  // blocks of 64 inputs
+          if (h == 1 && w == 8) break;
+          // All eight gathers of a block are issued before the first is used.
+          uint4 c1[8];
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            const int g = 4 * c + g4;
+          for (int g = 0; g < 8; ++g) {
             uint32_t i1;
-            if (k16)
-              i1 = ((g4 < 2 ? v0 : v1) >> (16 * (g4 & 1))) & 0xFFFFu;
+            if constexpr (k16)
+              i1 = (lo[4 * h + (g >> 1)] >> (16 * (g & 1))) & 0xFFFFu;
             else
-              i1 = ((low >> (8 * g4)) & 0xFFu) | (((hi4w >> (4 * g)) & 15u) << 8);
-            const uint4 c1 = kBook ? cb1s[i1] : __ldg(reinterpret_cast<const uint4*>(l.cb1) + i1);
-            if constexpr (kLadder) {
-              float v[8];
-              ladder_sum(l, res, g, c1, cb1s, v);
-              pack_scaled<T>(v, scf, out + 4 * g4);
-            } else {
-              uint32_t c2[4] = {0, 0, 0, 0};
-              if (kTwo) {
-                const int i2 = (int)((s24w >> (4 * g)) & 15u);
-#pragma unroll
-                for (int w4 = 0; w4 < 4; ++w4) c2[w4] = __shfl_sync(0xffffffffu, cb2r[w4], i2);
-              }
-              decode_scaled<T, kTwo>(c1, c2, sc, out + 4 * g4);
-            }
+              i1 = ((lo[2 * h + (g >> 2)] >> (8 * (g & 3))) & 0xFFu) | (((hi[h] >> (4 * g)) & 15u) << 8);
+            c1[g] = kBook ? cb1s[i1] : __ldg(reinterpret_cast<const uint4*>(l.cb1) + i1);
           }
-          ptx::tmem_st16(ta + 16u * c, out);
+          LadderIdx res{};
+          if constexpr (kLadder)
+            if (valid) load_ladder_block(l, (int64_t)16 * j * N + (int64_t)r * w + 8 * h, res);
+          const unsigned short sc = (unsigned short)(h ? sc2 >> 16 : sc2);
+          const float scf = kLadder ? __half2float(__ushort_as_half(sc)) : 0.f;
+          if (!waited) {
+            waited = true;
+            if (!ptx::mbar_wait(empty_a(part), (round - 1) & 1, a.err)) ok = false;
+            ptx::tc_fence_after();
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {  // 4 groups (16 TMEM columns) at a time
+            uint32_t out[16];
+#pragma unroll
+            for (int g4 = 0; g4 < 4; ++g4) {
+              const int g = 4 * c + g4;
+              if constexpr (kLadder) {
+                float v[8];
+                ladder_sum(l, res, g, c1[g], cb1s, v);
+                pack_scaled<T>(v, scf, out + 4 * g4);
+              } else {
+                uint32_t c2[4] = {0, 0, 0, 0};
+                if (kTwo) {
+                  const int i2 = (int)(s2[h] >> (4 * g));  // the shuffle takes it modulo 16
+#pragma unroll
+                  for (int w4 = 0; w4 < 4; ++w4) c2[w4] = __shfl_sync(0xffffffffu, cb2r[w4], i2, 16);
+                }
+                decode_scaled<T, kTwo>(c1[g], c2, sc, out + 4 * g4);
+              }
+            }
+            ptx::tmem_st16(ta + 32u * h + 16u * c, out);
+          }
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
+        if (!ok) break;
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(full_a(st));
-      }
-      it0 += nkb;
-      js0 += nsl;
-
-      // ---------------------------------------------------------- epilogue
-      const int b = ui % nacc;
-      if (ok && (*abort_flag || !ptx::mbar_wait(acc_full(b), (ui / nacc) & 1, a.err))) ok = false;
-      if (!ok) break;
-      ptx::tc_fence_after();
-      const float bv = (a.bias && valid) ? Elt<T>::to_f32(a.bias[(int64_t)t.e * N + r]) : 0.f;
-      for (int c0 = 16 * part; c0 < t.n; c0 += 16 * kXtParts) {
-        uint32_t v[16];
-        ptx::tmem_ld16(tlane + acols * b + c0, v);
-        ptx::tmem_wait_ld();
-        const int left = t.n - c0;
-        float f[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]) + bv;
-        uint16_t* y = a.y + (int64_t)(t.first + c0) * a.Nout + n;
-        if (!a.glu) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (valid && i < left) y[(int64_t)i * a.Nout] = Elt<T>::from_f32(apply_act(a.act, f[i]));
-        } else {
-          // gate lanes finish the even token of each pair, up lanes the odd one
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, is_up ? f[i] : f[i + 1], 16);
-            const float gate = is_up ? other : f[i], up = is_up ? f[i + 1] : other;
-            const int tok = is_up ? i + 1 : i;
-            if (valid && tok < left) y[(int64_t)tok * a.Nout] = Elt<T>::from_f32(gated(a.act, gate, up));
-          }
+        if (lane == 0) ptx::mbar_arrive(full_a(part));
+        if (pending) {
+          ok = finish_tile(prev, ui - 1);
+          pending = false;
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(acc_empty(b));
+      js0 += nsl;
+      if (ok && pending) ok = finish_tile(prev, ui - 1);  // no block of this tile was this warp's
+      prev = t;
+      pending = ok;
     }
+    if (ok && pending) ok = finish_tile(prev, ui - 1);
     if (!ok) *abort_flag = 1;
   }
 
@@ -497,7 +562,7 @@ static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, c
   const int smem = (int)xt_smem(Tmax);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int nacc = 2 * ((Tmax + 31) / 32 * 32) + kXtStages * (int)kXtACols <= 512 ? 2 : 1;
+  const int nacc = 2 * ((Tmax + 31) / 32 * 32) + kXtParts * (int)kXtACols <= 512 ? 2 : 1;
   cfg.gridDim = dim3(num_sms);
   cfg.blockDim = dim3(kXtThreads);
   cfg.dynamicSmemBytes = smem;
