@@ -2,11 +2,13 @@
 // act(x[rows[r]] . W_e^T + b) on the tensor cores, W decoded into tensor memory.
 //
 // A persistent block per SM walks tiles of 128 rows of W (glu: 64 gate rows and the 64 up
-// rows that go with them) x up to Tmax rows of x, over all of K.  The tiles of all experts are
-// numbered in expert order (find_tiles) and cut into one contiguous, equal range per block, so
-// a block changes its expert, and with it the codebook in shared memory, once or twice.
-//   warp 0     lane 0: x, per 64-wide k block, TMA loads of the tile's x rows (32 rows a copy,
-//              128-byte swizzle) into a ring of S stages
+// rows that go with them) x up to Tmax rows of x, over all of K; an expert's rows are spread
+// evenly over its tiles.  The tiles of all experts are numbered in expert order (find_tiles) and
+// cut into one contiguous range of equal cost per block, so a block changes its expert, and with
+// it the codebook in shared memory, once or twice.
+//   warp 0     lane 0: x, per 64-wide k block, one TMA load of the tile's x rows (a box of 64, 128
+//              or 256 rows, 128-byte swizzle) into a ring of S stages.  One large box matters: eight
+//              boxes of 32 rows cost 660 ns a block instead of 480
 //   warp 1     allocates TMEM; lane 0 issues tcgen05.mma (M = 128, N = the tile's rows rounded
 //              up to 16, K = 16), A from TMEM, B from shared memory, and commits each stage
 //   warp 2     lane 0: the expert's 12-bit codebook (one bulk copy when it changes) and, per
@@ -47,10 +49,16 @@ constexpr uint32_t kXtOffTiles = 65536;                // after the codebook
 constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 16;
 constexpr uint32_t kXtOffIdx = kXtOffBars + 512;
 constexpr uint32_t kXtOffX = (kXtOffIdx + kXtSlots * kXtIdxSlot + 1023) / 1024 * 1024;
+// Tmax is 64, 128 or 256 (the boxes' heights).
 constexpr uint32_t xt_smem(int Tmax) { return kXtOffX + kXtStages * Tmax * 128u + 1024u; }
 static_assert(xt_smem(kXtMaxT) <= 232448, "shared memory of the widest tile");
 
-constexpr int kXtBox = 32;  // x rows of one TMA load
+constexpr int kXtBoxes = 3;        // x rows of one TMA load: 64, 128 or 256
+constexpr int kXtTileCost = 600;   // cost of a tile's decode, in x rows (13.6 us + 23 ns a row at K = 2048)
+
+struct XtMaps {
+  CUtensorMap x[kXtBoxes];
+};
 
 // xs[r] = x[rows[r]], zeros where the row is out of range.  One block per row.
 __global__ void __launch_bounds__(128) gather_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ rows,
@@ -70,7 +78,7 @@ struct XtTile {
 
 template <int FMT, typename T, bool kStaged>
 __global__ void __launch_bounds__(kXtThreads, 1)
-    experts_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ ExpertsArgs a, int Tmax,
+    experts_tc_kernel(const __grid_constant__ XtMaps maps, const __grid_constant__ ExpertsArgs a, int Tmax,
                       int nacc) {
   extern __shared__ unsigned char smem_raw[];
   constexpr bool k16 = (FMT == kFmtVq16 || FMT == kFmtVq16Rvq);
@@ -141,8 +149,49 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   find_tiles(a, Tmax, RT, tiles, part_sums, kXtThreads);
-  const int total = tiles.start[a.E];
-  const int ubeg = (int)((int64_t)total * blockIdx.x / gridDim.x), uend = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  // Rows of each of expert e's tiles: even, a multiple of 16.
+  auto tile_rows = [&](int e) {
+    const int n = tiles.off[e + 1] - tiles.off[e], tt = (n + Tmax - 1) / Tmax;
+    return tt == 0 ? 0 : ((n + tt - 1) / tt + 15) & ~15;
+  };
+  // The block's tiles.  Expert e's tiles cost kXtTileCost + their rows each; the tile at which a share
+  // of the whole cost is reached ends one block's range and starts the next one's.
+  float* cost = reinterpret_cast<float*>(sm + kXtOffX);  // [E + 1], in the x area before its first use
+  if (warp == 0) {
+    float run = 0.f;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const float c = e < a.E ? (float)(tiles.start[e + 1] - tiles.start[e]) * (float)(kXtTileCost + tile_rows(e)) : 0.f;
+      float sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (e < a.E) cost[e] = run + sum - c;
+      run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) cost[a.E] = run;
+    __syncwarp();
+    if (lane < 2) {
+      const int b = blockIdx.x + lane;
+      int u = b == 0 ? 0 : tiles.start[a.E];
+      if (b > 0 && b < (int)gridDim.x) {
+        const float c = run * ((float)b / (float)gridDim.x);
+        int lo = 0, hi = a.E;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (cost[mid] <= c) lo = mid; else hi = mid;
+        }
+        const int k = (int)((c - cost[lo]) / (float)(kXtTileCost + tile_rows(lo)));
+        u = tiles.start[lo] + max(0, min(k, tiles.start[lo + 1] - tiles.start[lo]));
+      }
+      part_sums[lane] = u;
+    }
+    ptx::fence_proxy_async_smem();  // TMA writes the x area next
+  }
+  __syncthreads();
+  const int ubeg = part_sums[0], uend = part_sums[1];
 
   // Tile u; `e` walks along (it starts at the range's first expert).
   int e_walk = ubeg < uend ? expert_of(tiles, a.E, ubeg) : 0;
@@ -154,8 +203,9 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     const int local = u - tiles.start[e_walk];
     t.rt = local / tt;
     const int tk = local - t.rt * tt;
-    t.first = beg + tk * Tmax;
-    t.n = min(Tmax, n - tk * Tmax);
+    const int rows = tile_rows(e_walk);
+    t.first = beg + tk * rows;
+    t.n = min(rows, n - tk * rows);
     t.T = (t.n + 15) & ~15;
     return t;
   };
@@ -163,12 +213,12 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ x rows
     if (lane == 0) {
-      ptx::prefetch_tensormap(&xmap);
       int it = 0;
       bool ok = true;
       for (int u = ubeg; ok && u < uend; ++u) {
         const XtTile t = tile_of(u);
-        const int boxes = (t.n + kXtBox - 1) / kXtBox;  // rows past the tile's are loaded and not used
+        const int box = t.T <= 64 ? 64 : t.T <= 128 ? 128 : 256;  // rows past the tile's are loaded and not used
+        const CUtensorMap* map = &maps.x[box >> 7];
         for (int kb = 0; kb < nkb; ++kb) {
           const int s = it % kSt;
           if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty_b(s), ((it / kSt) - 1) & 1, a.err))) {
@@ -176,9 +226,8 @@ __global__ void __launch_bounds__(kXtThreads, 1)
             ok = false;
             break;
           }
-          ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)(boxes * kXtBox) * 128u);
-          for (int b = 0; b < boxes; ++b)
-            ptx::tma_load_2d(b_tile(s) + (uint32_t)(b * kXtBox) * 128u, &xmap, 64 * kb, t.first + kXtBox * b, full_b(s));
+          ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)box * 128u);
+          ptx::tma_load_2d(b_tile(s), map, 64 * kb, t.first, full_b(s));
           ++it;
         }
       }
@@ -547,17 +596,20 @@ static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, c
     a.rows = nullptr;
     a.x_rows = a.T;
   }
-  CUtensorMap map;
+  XtMaps maps;
   const CUtensorMapDataType dt =
       a.w.act == VQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t dims[2] = {(cuuint64_t)a.w.K, (cuuint64_t)a.x_rows};
   const cuuint64_t strides[1] = {(cuuint64_t)a.w.K * 2};
-  const cuuint32_t box[2] = {64, kXtBox};
   const cuuint32_t estr[2] = {1, 1};
-  if (enc(&map, dt, 2, const_cast<uint16_t*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  for (int i = 0; i < kXtBoxes; ++i) {
+    const int rows = 64 << i;  // a tile of at most Tmax rows never takes a larger box than Tmax
+    const cuuint32_t box[2] = {64, (cuuint32_t)(rows < Tmax ? rows : Tmax)};
+    if (enc(&maps.x[i], dt, 2, const_cast<uint16_t*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
   auto kern = experts_tc_kernel<FMT, T, kStaged>;
   const int smem = (int)xt_smem(Tmax);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -566,7 +618,7 @@ static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, c
   cfg.gridDim = dim3(num_sms);
   cfg.blockDim = dim3(kXtThreads);
   cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, kern, map, a, Tmax, nacc);
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, Tmax, nacc);
 }
 
 template <typename T>
