@@ -40,7 +40,7 @@ constexpr int kXtRows = 128;
 constexpr int kXtParts = 4;                            // decode warps per TMEM lane quarter, and A stages
 constexpr int kXtDecode = 4 * kXtParts;                // decode warps
 constexpr int kXtThreads = 32 * (4 + kXtDecode);
-constexpr int kXtStages = 4;                           // x stages of 64 inputs
+constexpr int kXtStages = 2;                           // x stages of a slice (128 inputs)
 constexpr int kXtMaxT = 256;
 constexpr int kXtSlots = kXtParts;                     // index slices in flight
 constexpr uint32_t kXtACols = 64;                      // TMEM columns of one A stage (128 k of 16-bit pairs)
@@ -50,7 +50,7 @@ constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 
 constexpr uint32_t kXtOffIdx = kXtOffBars + 512;
 constexpr uint32_t kXtOffX = (kXtOffIdx + kXtSlots * kXtIdxSlot + 1023) / 1024 * 1024;
 // Tmax is 64, 128 or 256 (the boxes' heights).
-constexpr uint32_t xt_smem(int Tmax) { return kXtOffX + kXtStages * Tmax * 128u + 1024u; }
+constexpr uint32_t xt_smem(int Tmax) { return kXtOffX + kXtStages * Tmax * 256u + 1024u; }
 static_assert(xt_smem(kXtMaxT) <= 232448, "shared memory of the widest tile");
 
 constexpr int kXtBoxes = 3;        // x rows of one TMA load: 64, 128 or 256
@@ -69,6 +69,30 @@ __global__ void __launch_bounds__(128) gather_rows_kernel(const uint4* __restric
   const bool in = xr >= 0 && xr < x_rows;
   for (int i = threadIdx.x; i < K8; i += 128) xs[r * K8 + i] = in ? x[(int64_t)xr * K8 + i] : make_uint4(0, 0, 0, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+
+// Lane-wise wait of a warp: every lane with `wait` polls its own barrier until all are through.
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, bool wait, volatile int* abort_flag,
+                                           uint32_t* err) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < kWaitSpinLimit; ++i) {
+    const bool ok = !wait || ptx::mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((i & 63u) == 63u) {
+      const uint64_t t = ptx::globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (__any_sync(0xffffffffu, *abort_flag || t - t0 > 1000000000ull)) break;
+    }
+  }
+  if (err && (threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
+  return false;
 }
 
 // One tile: its expert, its place, its x rows.
@@ -94,7 +118,6 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   ExpertTiles& tiles = *reinterpret_cast<ExpertTiles*>(sm + kXtOffTiles);
   const uint32_t bar0 = base + kXtOffBars;
   auto full_b = [&](int s) { return bar0 + 8u * s; };
-  auto empty_b = [&](int s) { return bar0 + 8u * (kSt + s); };
   auto acc_full = [&](int b) { return bar0 + 8u * (2 * kSt + b); };
   auto acc_empty = [&](int b) { return bar0 + 8u * (2 * kSt + 2 + b); };
   const uint32_t cb_full = bar0 + 8u * (2 * kSt + 4), cb_empty = cb_full + 8u, bar1 = cb_full + 16u;
@@ -107,12 +130,12 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kXtOffBars + 260);
   int* part_sums = reinterpret_cast<int*>(sm + kXtOffBars + 264);  // 2 per warp
   static_assert(264 + 8 * kXtThreads / 32 <= 512, "scan area");
-  const uint32_t b_bytes = (uint32_t)Tmax * 128u;
-  auto b_tile = [&](int s) { return base + kXtOffX + b_bytes * s; };
+  const uint32_t b_bytes = (uint32_t)Tmax * 128u;  // 64 inputs of the tile's rows
+  auto b_tile = [&](int s, int h) { return base + kXtOffX + b_bytes * (2 * s + h); };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int N = a.w.N, K = a.w.K, G = K / 8;
-  const int nkb = K / 64, nsl = (K + 127) / 128;
+  const int nsl = (K + 127) / 128;
   const int out_tile = a.glu ? kXtRows / 2 : kXtRows;  // columns of y of a tile
   const int RT = (a.Nout + out_tile - 1) / out_tile;
   const uint32_t acols = ((uint32_t)Tmax + 31u) & ~31u;
@@ -121,8 +144,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kSt; ++s) {
-      ptx::mbar_init(full_b(s), 1);   // the x warp's expect_tx arrival (+ bytes)
-      ptx::mbar_init(empty_b(s), 1);  // one tcgen05.commit
+      ptx::mbar_init(full_b(s), 1);  // the x warp's expect_tx arrival (+ bytes)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(acc_full(b), 1);
@@ -213,77 +235,83 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ x rows
     if (lane == 0) {
-      int it = 0;
+      int js = 0;
       bool ok = true;
       for (int u = ubeg; ok && u < uend; ++u) {
         const XtTile t = tile_of(u);
         const int box = t.T <= 64 ? 64 : t.T <= 128 ? 128 : 256;  // rows past the tile's are loaded and not used
         const CUtensorMap* map = &maps.x[box >> 7];
-        for (int kb = 0; kb < nkb; ++kb) {
-          const int s = it % kSt;
-          if (*abort_flag || (it >= kSt && !ptx::mbar_wait(empty_b(s), ((it / kSt) - 1) & 1, a.err))) {
+        for (int j = 0; j < nsl; ++j, ++js) {
+          const int s = js % kSt, before = js - kSt;  // the slice that the stage held
+          if (before >= 0 && !ptx::mbar_wait(empty_a(before % kXtParts), (before / kXtParts) & 1, a.err)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
-          ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)box * 128u);
-          ptx::tma_load_2d(b_tile(s), map, 64 * kb, t.first, full_b(s));
-          ++it;
+          const int blocks = slice_width(j, G) / 8;
+          ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)(blocks * box) * 128u);
+          for (int h = 0; h < blocks; ++h) ptx::tma_load_2d(b_tile(s, h), map, 128 * j + 64 * h, t.first, full_b(s));
         }
       }
       // Do not leave while a copy into this block's shared memory may be in flight.
-      for (int i = it > kSt ? it - kSt : 0; i < it; ++i) ptx::mbar_wait(full_b(i % kSt), (i / kSt) & 1, a.err);
+      for (int i = js > kSt ? js - kSt : 0; i < js; ++i) ptx::mbar_wait(full_b(i % kSt), (i / kSt) & 1, a.err);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kAbFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      bool ok = true;
-      int it = 0, js = 0, ui = 0;
-      for (int u = ubeg; ok && u < uend; ++u, ++ui) {
-        const XtTile t = tile_of(u);
-        const uint32_t idesc = ptx::idesc_f16(kAbFmt, kXtRows, (uint32_t)t.T);
-        const int b = ui % nacc;
-        const uint32_t acc = tmem + acols * b;
-        // the decode warps have read the buffer's last tile
-        if (*abort_flag || (ui >= nacc && !ptx::mbar_wait(acc_empty(b), ((ui / nacc) - 1) & 1, a.err))) {
+    // The whole warp walks the tiles and waits, and one elected lane issues: with warp-uniform
+    // control flow the descriptors are in uniform registers, as tcgen05.mma takes them.  Issued
+    // from a loop of one lane, an MMA took 80 to 120 cycles and set the kernel's pace.
+    constexpr uint32_t kAbFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+    bool ok = true;
+    int js = 0, ui = 0;
+    for (int u = ubeg; ok && u < uend; ++u, ++ui) {
+      const XtTile t = tile_of(u);
+      const uint32_t idesc = __shfl_sync(0xffffffffu, ptx::idesc_f16(kAbFmt, kXtRows, (uint32_t)t.T), 0);
+      const int b = ui % nacc;
+      const uint32_t acc = utmem + acols * b;
+      for (int j = 0; j < nsl; ++j, ++js) {
+        const int st = js % kXtParts, s = js % kSt;
+        // One poll for all that the slice waits for, a barrier a lane: the decode's gathers keep the
+        // shared-memory pipe's queue long, and every poll goes through it (250 to 500 cycles).
+        uint32_t bar = full_a(st), par = (uint32_t)(js / kXtParts) & 1u;
+        bool wait = lane == 0;
+        if (lane == 1) {
+          bar = full_b(s);
+          par = (uint32_t)(js / kSt) & 1u;
+          wait = true;
+        }
+        if (lane == 2 && j == 0 && ui >= nacc) {  // the decode warps have read the accumulator's last tile
+          bar = acc_empty(b);
+          par = (uint32_t)((ui / nacc) - 1) & 1u;
+          wait = true;
+        }
+        if (!wait_lanes(bar, par, wait, abort_flag, a.err)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        for (int kb = 0; ok && kb < nkb; ++js) {
-          const int st = js % kXtParts;
-          if (*abort_flag || !ptx::mbar_wait(full_a(st), (js / kXtParts) & 1, a.err)) {
-            ok = false;
-            break;
-          }
-          const uint32_t at = tmem + acol0 + kXtACols * st;
+        const uint32_t at = utmem + acol0 + kXtACols * st;
+        const uint64_t b0 = ptx::smem_desc_sw128(b_tile(s, 0)), b1 = ptx::smem_desc_sw128(b_tile(s, 1));
+        const bool two = slice_width(j, G) == 16;
+        if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // the slice's blocks of 64 inputs
-            if (kb >= nkb) break;
-            const int s = it % kSt;
-            if (!ptx::mbar_wait(full_b(s), (it / kSt) & 1, a.err)) {
-              ok = false;
-              break;
-            }
-            ptx::tc_fence_after();
-            const uint64_t bd = ptx::smem_desc_sw128(b_tile(s));
+          for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
+            ptx::umma_f16_ts(acc, at + 8u * kk, b0 + 2u * kk, idesc, (j | kk) != 0);
+          if (two) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
-              ptx::umma_f16_ts(acc, at + 32u * h + 8u * kk, bd + 2u * kk, idesc, (kb | kk) != 0);
-            ptx::umma_commit(empty_b(s));
-            ++it;
-            ++kb;
+            for (int kk = 0; kk < 4; ++kk) ptx::umma_f16_ts(acc, at + 32u + 8u * kk, b1 + 2u * kk, idesc, 1u);
           }
-          if (ok) ptx::umma_commit(empty_a(st));
+          ptx::umma_commit(empty_a(st));  // frees the slice's A and x stages
+          if (j + 1 == nsl) ptx::umma_commit(acc_full(b));
         }
-        if (ok) ptx::umma_commit(acc_full(b));
+        __syncwarp();
       }
-      if (!ok) *abort_flag = 1;
-      // The last commit covers every MMA before it: wait for it, so that TMEM and shared memory
-      // are not released under one (on a whole run the decode warps have waited already).
-      if (it) ptx::mbar_wait(empty_b((it - 1) % kSt), ((it - 1) / kSt) & 1, a.err);
     }
+    if (!ok) *abort_flag = 1;
+    // The last commit covers every MMA before it: wait for it, so that TMEM and shared memory
+    // are not released under one (on a whole run the decode warps have waited already).
+    if (js) ptx::mbar_wait(empty_a((js - 1) % kXtParts), ((js - 1) / kXtParts) & 1, a.err);
   } else if (warp == 2) {
     // ------------------------------------------------------------ codebooks and index slices
     if (lane == 0 && (kBook || kStaged || kLadder)) {
@@ -294,7 +322,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         const XtTile t = tile_of(u);
         const LayerArgs l = expert_layer(a, t.e);
         if ((kBook || (kLadder && a.w.n8)) && (books == 0 || (!a.shared && t.e != last_e))) {
-          if (*abort_flag || (books > 0 && !ptx::mbar_wait(cb_empty, (books - 1) & 1, a.err))) {
+          if (books > 0 && !ptx::mbar_wait(cb_empty, (books - 1) & 1, a.err)) {
             ok = false;
             break;
           }
@@ -313,7 +341,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         const int r0 = out_tile * t.rt, nr = min(out_tile, a.Nout - r0), runs = a.glu ? 2 : 1;
         for (int j = 0; j < nsl; ++j, ++js) {
           const int sl = js % kXtSlots;
-          if (*abort_flag || (js >= kXtSlots && !ptx::mbar_wait(idx_empty(sl), ((js / kXtSlots) - 1) & 1, a.err))) {
+          if (js >= kXtSlots && !ptx::mbar_wait(idx_empty(sl), ((js / kXtSlots) - 1) & 1, a.err)) {
             ok = false;
             break;
           }
@@ -364,7 +392,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
       const bool valid = n < a.Nout;
       const int r = is_up ? a.Nout + n : n;
       const int b = ui % nacc;
-      if (*abort_flag || !ptx::mbar_wait(acc_full(b), (ui / nacc) & 1, a.err)) return false;
+      if (!ptx::mbar_wait(acc_full(b), (ui / nacc) & 1, a.err)) return false;
       ptx::tc_fence_after();
       const float bv = (a.bias && valid) ? Elt<T>::to_f32(a.bias[(int64_t)t.e * N + r]) : 0.f;
       for (int c0 = 16 * part; c0 < t.n; c0 += 16 * kXtParts) {
@@ -418,7 +446,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(cb_empty);
           }
-          if (*abort_flag || !ptx::mbar_wait(cb_full, books & 1, a.err)) ok = false;
+          if (!ptx::mbar_wait(cb_full, books & 1, a.err)) ok = false;
         }
         ++books;
       }
@@ -428,7 +456,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
       const uint32_t ta = tlane + acol0 + kXtACols * (uint32_t)part;
       for (int j = (part + kXtParts - js0 % kXtParts) % kXtParts; ok && j < nsl; j += kXtParts) {
         const int w = slice_width(j, G), round = (js0 + j) / kXtParts;
-        if (*abort_flag || (kStaged && !ptx::mbar_wait(idx_full(part), round & 1, a.err))) {
+        if (kStaged && !ptx::mbar_wait(idx_full(part), round & 1, a.err)) {
           ok = false;
           break;
         }
