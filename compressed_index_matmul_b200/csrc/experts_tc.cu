@@ -1,21 +1,25 @@
 // Products grouped by expert for many rows per expert (vq_experts_forward): y[r] =
 // act(x[rows[r]] . W_e^T + b) on the tensor cores, W decoded into tensor memory.
 //
-// A persistent block per SM walks tiles of 128 rows of W (glu: 64 gate rows and the 64 up
-// rows that go with them) x up to Tmax rows of x, over all of K; an expert's rows are spread
-// evenly over its tiles.  The tiles of all experts are numbered in expert order (find_tiles) and
-// cut into one contiguous range of equal cost per block, so a block changes its expert, and with
-// it the codebook in shared memory, once or twice.
-//   warp 0     lane 0: x, per 64-wide k block, one TMA load of the tile's x rows (a box of 64, 128
-//              or 256 rows, 128-byte swizzle) into a ring of S stages.  One large box matters: eight
-//              boxes of 32 rows cost 660 ns a block instead of 480
-//   warp 1     allocates TMEM; lane 0 issues tcgen05.mma (M = 128, N = the tile's rows rounded
-//              up to 16, K = 16), A from TMEM, B from shared memory, and commits each stage
-//   warp 2     lane 0: the expert's 12-bit codebook (one bulk copy when it changes) and, per
-//              128-input slice, the tile's index bytes (one contiguous run per plane; glu: two)
-//              into a ring of slots
-//   warps 4..  decode: four per TMEM lane quarter; thread = one row of the tile (its lane).
-//              Slice `js` of the block's whole sequence goes to warp js % 4 of every quarter, into A
+// A persistent pair of blocks (a cluster of two, one per SM) walks tiles of 256 rows of W (glu:
+// 128 gate rows and the 128 up rows that go with them) x up to Tmax rows of x, over all of K.
+// Each block decodes half of the tile's rows of W and holds half of its x rows in shared memory;
+// tcgen05.mma.cta_group::2 multiplies both, so an SM reads half of the x that a tile of its
+// own would need (with tiles per block the x loads, 32 KiB per 64 inputs and SM, ran at the
+// L2's 7 TB/s and set the pace).  The tiles of all experts are numbered in expert order
+// (find_tiles) and cut into one contiguous, equal range per pair, so a pair changes its
+// expert, and with it the codebook in shared memory, once or twice.
+//   warp 0     lane 0: x, per 64-wide k block, TMA loads of the block's half of the tile's x rows (32
+//              rows a copy, 128-byte swizzle) into a ring of S stages
+//   warp 1     allocates TMEM; lane 0 of the first block issues tcgen05.mma (M = 256, N = the
+//              tile's rows rounded up to 16, K = 16), A from both blocks' TMEM, B from both
+//              blocks' shared memory, and commits each stage to both; lane 0 of the second passes
+//              its x stages' arrivals on
+//   warp 2     the expert's 12-bit codebook (one bulk copy when it changes) and, per
+//              128-input slice, the index bytes of the block's rows (one contiguous run per
+//              plane; glu: two) into a ring of slots
+//   warps 4..  decode: four per TMEM lane quarter; thread = one row of W (its lane).
+//              Slice `js` of the pair's whole sequence goes to warp js % 4 of every quarter, into A
 //              stage js % 4 (64 TMEM columns, 128 inputs).  After a tile's last slice the same
 //              threads read the accumulator, apply bias and activation and store y: consecutive
 //              lanes are consecutive columns, and rows past the expert's last are not written.
@@ -23,9 +27,9 @@
 // of the next are already on their way.  With Tmax <= 128 the accumulator has two buffers, so
 // the MMAs of the next tile need not wait for the stores either.
 // Rows that come through `rows` are first copied into row order (gather_rows_kernel): T K
-// elements written and read once more, 15 us of the 300 us of a 16384 x 2048 gather into
-// 4096 x 2048 weights.  Gathering them in the x loads instead (TMA tile::gather4) took 40 ns per
-// four rows, 2.6 us a k block of 256 rows against the 0.5 us that its decode takes.
+// elements written and read once more, 15 us of a 16384 x 2048 gather.  Gathering them in the x
+// loads instead (TMA tile::gather4) took 40 ns per four rows, 2.6 us a k block of 256 rows,
+// several times what its decode takes.
 // Every mbarrier wait is bounded; a timeout sets the handle's error word, and the block winds
 // down (waits for its own copies and MMAs, frees TMEM).
 #include <cuda.h>
@@ -40,20 +44,26 @@ constexpr int kXtRows = 128;
 constexpr int kXtParts = 4;                            // decode warps per TMEM lane quarter, and A stages
 constexpr int kXtDecode = 4 * kXtParts;                // decode warps
 constexpr int kXtThreads = 32 * (4 + kXtDecode);
-constexpr int kXtStages = 2;                           // x stages of a slice (128 inputs)
+constexpr int kXtStages = 4;                           // x stages of a slice (128 inputs)
 constexpr int kXtMaxT = 256;
 constexpr int kXtSlots = kXtParts;                     // index slices in flight
 constexpr uint32_t kXtACols = 64;                      // TMEM columns of one A stage (128 k of 16-bit pairs)
 constexpr uint32_t kXtIdxHi = 2048, kXtIdxS2 = 3072, kXtIdxSc = 4096, kXtIdxSlot = 4608;
 constexpr uint32_t kXtOffTiles = 65536;                // after the codebook
 constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 16;
-constexpr uint32_t kXtOffIdx = kXtOffBars + 512;
+constexpr uint32_t kXtOffIdx = kXtOffBars + 768;
 constexpr uint32_t kXtOffX = (kXtOffIdx + kXtSlots * kXtIdxSlot + 1023) / 1024 * 1024;
 // Tmax is 64, 128 or 256 (the boxes' heights).
-constexpr uint32_t xt_smem(int Tmax) { return kXtOffX + kXtStages * Tmax * 256u + 1024u; }
+// At least 144 KiB, so that no other kernel of this library that allocates TMEM (94 KiB and more a
+// block) shares the SM: a pair takes all 512 columns of both SMs, and two pairs that each hold one
+// SM's TMEM and wait for the other's would never go on.
+constexpr uint32_t xt_smem(int Tmax) {
+  const uint32_t need = kXtOffX + kXtStages * (Tmax / 2) * 256u + 1024u;
+  return need < 147456u ? 147456u : need;
+}
 static_assert(xt_smem(kXtMaxT) <= 232448, "shared memory of the widest tile");
 
-constexpr int kXtBoxes = 3;        // x rows of one TMA load: 64, 128 or 256
+constexpr int kXtBoxes = 3;        // x rows of one TMA load: 32, 64 or 128
 constexpr int kXtTileCost = 600;   // cost of a tile's decode, in x rows (13.6 us + 23 ns a row at K = 2048)
 
 struct XtMaps {
@@ -76,6 +86,39 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
   return p != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Arrive on a barrier of block `rank` of the pair.  What the arrivals tell of is in TMEM and in the
+// async proxy's shared memory, ordered by the tcgen05 fences, so the cheap default scope serves (a
+// release at cluster scope held each decode warp up for more than 1000 cycles).
+__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ptx::map_shared_rank(bar, rank)) : "memory");
+}
+// The pair's TMEM and MMA (cta_group::2; both blocks allocate and free).
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive once on `bar` of both blocks when every MMA this thread issued before has completed.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"((unsigned short)3)
+               : "memory");
 }
 
 // Lane-wise wait of a warp: every lane with `wait` polls its own barrier until all are through.
@@ -125,19 +168,21 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   auto empty_a = [&](int s) { return bar1 + 8u * (kXtParts + s); };
   auto idx_full = [&](int s) { return bar1 + 8u * (2 * kXtParts + s); };
   auto idx_empty = [&](int s) { return bar1 + 8u * (3 * kXtParts + s); };
-  static_assert(8 * (2 * kSt + 6 + 4 * kXtParts) <= 256, "barriers overlap the flags");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kXtOffBars + 256);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kXtOffBars + 260);
-  int* part_sums = reinterpret_cast<int*>(sm + kXtOffBars + 264);  // 2 per warp
-  static_assert(264 + 8 * kXtThreads / 32 <= 512, "scan area");
-  const uint32_t b_bytes = (uint32_t)Tmax * 128u;  // 64 inputs of the tile's rows
+  auto peer_b = [&](int s) { return bar1 + 8u * (4 * kXtParts + s); };  // the second block's x stage (first block only)
+  static_assert(8 * (3 * kSt + 6 + 4 * kXtParts) <= 384, "barriers overlap the flags");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kXtOffBars + 384);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kXtOffBars + 388);
+  int* part_sums = reinterpret_cast<int*>(sm + kXtOffBars + 392);  // 2 per warp
+  static_assert(392 + 8 * kXtThreads / 32 <= 768, "scan area");
+  const uint32_t b_bytes = (uint32_t)(Tmax / 2) * 128u;  // 64 inputs of the block's half of the tile's rows
   auto b_tile = [&](int s, int h) { return base + kXtOffX + b_bytes * (2 * s + h); };
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int N = a.w.N, K = a.w.K, G = K / 8;
   const int nsl = (K + 127) / 128;
-  const int out_tile = a.glu ? kXtRows / 2 : kXtRows;  // columns of y of a tile
-  const int RT = (a.Nout + out_tile - 1) / out_tile;
+  const int out_tile = a.glu ? kXtRows / 2 : kXtRows;  // columns of y of the block's half of a tile
+  const uint32_t rank = __shfl_sync(0xffffffffu, cluster_rank(), 0);
+  const int RT = (a.Nout + 2 * out_tile - 1) / (2 * out_tile);  // row tiles of the pair
   const uint32_t acols = ((uint32_t)Tmax + 31u) & ~31u;
   const uint32_t acol0 = acols * nacc;  // then the A stages
   const uint32_t tcols = 512u;  // acol0 + kXtParts * kXtACols is above 256
@@ -145,15 +190,16 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kSt; ++s) {
       ptx::mbar_init(full_b(s), 1);  // the x warp's expect_tx arrival (+ bytes)
+      ptx::mbar_init(peer_b(s), 1);  // passed on by the second block
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(acc_full(b), 1);
-      ptx::mbar_init(acc_empty(b), kXtDecode);
+      ptx::mbar_init(acc_empty(b), 2 * kXtDecode);  // both blocks' decode warps (first block only)
     }
     ptx::mbar_init(cb_full, 1);
     ptx::mbar_init(cb_empty, kXtDecode);
     for (int s = 0; s < kXtParts; ++s) {
-      ptx::mbar_init(full_a(s), 4);     // one decode warp per TMEM lane quarter
+      ptx::mbar_init(full_a(s), 8);     // one decode warp per TMEM lane quarter, both blocks (first block only)
       ptx::mbar_init(empty_a(s), 1);    // one tcgen05.commit
       ptx::mbar_init(idx_full(s), 1);
       ptx::mbar_init(idx_empty(s), 4);  // the warps that decode the slice
@@ -162,11 +208,11 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(smem_u32(tmem_slot), tcols);
-    ptx::tmem_relinquish();
+    pair_tmem_alloc(smem_u32(tmem_slot), tcols);
   }
   ptx::tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  ptx::cluster_sync();  // the barriers of both blocks are initialised
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -196,10 +242,10 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     if (lane == 0) cost[a.E] = run;
     __syncwarp();
     if (lane < 2) {
-      const int b = blockIdx.x + lane;
+      const int b = (int)(blockIdx.x / 2) + lane, pairs = (int)(gridDim.x / 2);
       int u = b == 0 ? 0 : tiles.start[a.E];
-      if (b > 0 && b < (int)gridDim.x) {
-        const float c = run * ((float)b / (float)gridDim.x);
+      if (b > 0 && b < pairs) {
+        const float c = run * ((float)b / (float)pairs);
         int lo = 0, hi = a.E;
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
@@ -223,8 +269,8 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     t.e = e_walk;
     const int beg = tiles.off[e_walk], n = tiles.off[e_walk + 1] - beg, tt = (n + Tmax - 1) / Tmax;
     const int local = u - tiles.start[e_walk];
-    t.rt = local / tt;
-    const int tk = local - t.rt * tt;
+    const int rp = local / tt, tk = local - rp * tt;
+    t.rt = 2 * rp + (int)rank;
     const int rows = tile_rows(e_walk);
     t.first = beg + tk * rows;
     t.n = min(rows, n - tk * rows);
@@ -239,8 +285,9 @@ __global__ void __launch_bounds__(kXtThreads, 1)
       bool ok = true;
       for (int u = ubeg; ok && u < uend; ++u) {
         const XtTile t = tile_of(u);
-        const int box = t.T <= 64 ? 64 : t.T <= 128 ? 128 : 256;  // rows past the tile's are loaded and not used
-        const CUtensorMap* map = &maps.x[box >> 7];
+        const int half = t.T / 2, first = t.first + (int)rank * half;
+        const int box = half <= 32 ? 32 : half <= 64 ? 64 : 128;  // rows past the half are loaded and not used
+        const CUtensorMap* map = &maps.x[box >> 6];
         for (int j = 0; j < nsl; ++j, ++js) {
           const int s = js % kSt, before = js - kSt;  // the slice that the stage held
           if (before >= 0 && !ptx::mbar_wait(empty_a(before % kXtParts), (before / kXtParts) & 1, a.err)) {
@@ -250,14 +297,14 @@ __global__ void __launch_bounds__(kXtThreads, 1)
           }
           const int blocks = slice_width(j, G) / 8;
           ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)(blocks * box) * 128u);
-          for (int h = 0; h < blocks; ++h) ptx::tma_load_2d(b_tile(s, h), map, 128 * j + 64 * h, t.first, full_b(s));
+          for (int h = 0; h < blocks; ++h) ptx::tma_load_2d(b_tile(s, h), map, 128 * j + 64 * h, first, full_b(s));
         }
       }
       // Do not leave while a copy into this block's shared memory may be in flight.
       for (int i = js > kSt ? js - kSt : 0; i < js; ++i) ptx::mbar_wait(full_b(i % kSt), (i / kSt) & 1, a.err);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer (the first block's)
     // The whole warp walks the tiles and waits, and one elected lane issues: with warp-uniform
     // control flow the descriptors are in uniform registers, as tcgen05.mma takes them.  Issued
     // from a loop of one lane, an MMA took 80 to 120 cycles and set the kernel's pace.
@@ -265,9 +312,19 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
     int js = 0, ui = 0;
-    for (int u = ubeg; ok && u < uend; ++u, ++ui) {
+    if (rank == 1) {  // tell the first block which of this block's x stages have landed
+      const int n = (uend - ubeg) * nsl;
+      for (; js < n; ++js) {
+        if (!ptx::mbar_wait(full_b(js % kSt), (js / kSt) & 1, a.err)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) arrive_at(peer_b(js % kSt), 0);
+      }
+    }
+    for (int u = ubeg; rank == 0 && ok && u < uend; ++u, ++ui) {
       const XtTile t = tile_of(u);
-      const uint32_t idesc = __shfl_sync(0xffffffffu, ptx::idesc_f16(kAbFmt, kXtRows, (uint32_t)t.T), 0);
+      const uint32_t idesc = __shfl_sync(0xffffffffu, ptx::idesc_f16(kAbFmt, 2 * kXtRows, (uint32_t)t.T), 0);
       const int b = ui % nacc;
       const uint32_t acc = utmem + acols * b;
       for (int j = 0; j < nsl; ++j, ++js) {
@@ -281,7 +338,12 @@ __global__ void __launch_bounds__(kXtThreads, 1)
           par = (uint32_t)(js / kSt) & 1u;
           wait = true;
         }
-        if (lane == 2 && j == 0 && ui >= nacc) {  // the decode warps have read the accumulator's last tile
+        if (lane == 2) {
+          bar = peer_b(s);
+          par = (uint32_t)(js / kSt) & 1u;
+          wait = true;
+        }
+        if (lane == 3 && j == 0 && ui >= nacc) {  // the decode warps have read the accumulator's last tile
           bar = acc_empty(b);
           par = (uint32_t)((ui / nacc) - 1) & 1u;
           wait = true;
@@ -297,25 +359,36 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
-            ptx::umma_f16_ts(acc, at + 8u * kk, b0 + 2u * kk, idesc, (j | kk) != 0);
+            pair_umma_ts(acc, at + 8u * kk, b0 + 2u * kk, idesc, (j | kk) != 0);
           if (two) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) ptx::umma_f16_ts(acc, at + 32u + 8u * kk, b1 + 2u * kk, idesc, 1u);
+            for (int kk = 0; kk < 4; ++kk) pair_umma_ts(acc, at + 32u + 8u * kk, b1 + 2u * kk, idesc, 1u);
           }
-          ptx::umma_commit(empty_a(st));  // frees the slice's A and x stages
-          if (j + 1 == nsl) ptx::umma_commit(acc_full(b));
+          pair_commit(empty_a(st));  // frees the slice's A and x stages
+          if (j + 1 == nsl) pair_commit(acc_full(b));
         }
         __syncwarp();
       }
     }
     if (!ok) *abort_flag = 1;
-    // The last commit covers every MMA before it: wait for it, so that TMEM and shared memory
-    // are not released under one (on a whole run the decode warps have waited already).
-    if (js) ptx::mbar_wait(empty_a((js - 1) % kXtParts), ((js - 1) / kXtParts) & 1, a.err);
+    // The last commit covers every MMA before it and lands in both blocks: wait for it, so that
+    // TMEM and shared memory are not released under one (on a whole run the decode warps have
+    // waited already).
+    if (js && (rank == 0 || ok)) ptx::mbar_wait(empty_a((js - 1) % kXtParts), ((js - 1) / kXtParts) & 1, a.err);
   } else if (warp == 2) {
     // ------------------------------------------------------------ codebooks and index slices
-    if (lane == 0 && (kBook || kStaged || kLadder)) {
+    // Lane 4 h + p copies plane p (lo or idx16, hi4, s2, scales) of run h of the tile's rows (glu: the
+    // gate rows and the up rows, 64 rows apart in the slot; else one run).  One lane issuing all
+    // the copies of a slice was slower than the decode.
+    if (kBook || kStaged || kLadder) {
       const bool block_scales = a.w.scale_group == 64;
+      const int run = lane >> 2, plane = lane & 3;
+      const bool mine = kStaged && run < (a.glu ? 2 : 1) &&
+                        (plane == 0 || (plane == 1 && !k16) || (plane == 2 && kTwo) || (plane == 3 && block_scales));
+      // bytes of a row and slice of 16 groups
+      const int row16 = plane == 0 ? (k16 ? 32 : 16) : plane == 3 ? 4 : 8;
+      const uint32_t off = plane == 0 ? 0u : plane == 1 ? kXtIdxHi : plane == 2 ? kXtIdxS2 : kXtIdxSc;
+      const uint32_t all16 = (k16 ? 32u : 24u + (kTwo ? 8u : 0u)) + (block_scales ? 4u : 0u);  // of all planes
       bool ok = true;
       int js = 0, books = 0, last_e = -1;
       for (int u = ubeg; ok && u < uend; ++u) {
@@ -326,19 +399,22 @@ __global__ void __launch_bounds__(kXtThreads, 1)
             ok = false;
             break;
           }
-          if (kBook) {
-            ptx::mbar_arrive_expect_tx(cb_full, 65536u);
-            ptx::bulk_load(base, l.cb1, 65536u, cb_full);
-          } else {
-            ptx::mbar_arrive_expect_tx(cb_full, 4096u);
-            ptx::bulk_load(base, l.cb8, 4096u, cb_full);
+          if (lane == 0) {
+            const uint32_t bytes = kBook ? 65536u : 4096u;
+            ptx::mbar_arrive_expect_tx(cb_full, bytes);
+            ptx::bulk_load(base, kBook ? l.cb1 : l.cb8, bytes, cb_full);
           }
+          __syncwarp();
           ++books;
         }
         last_e = t.e;
         if (!kStaged) continue;
-        // rows of W: one run of the tile's rows, or a gate run and an up run (64 rows apart in the slot)
-        const int r0 = out_tile * t.rt, nr = min(out_tile, a.Nout - r0), runs = a.glu ? 2 : 1;
+        const int r0 = out_tile * t.rt, nr = max(0, min(out_tile, a.Nout - r0)), runs = a.glu ? 2 : 1;
+        const unsigned char* src = plane == 0   ? (k16 ? reinterpret_cast<const unsigned char*>(l.idx16) : l.lo)
+                                   : plane == 1 ? l.hi4
+                                   : plane == 2 ? l.s2
+                                                : reinterpret_cast<const unsigned char*>(l.scales);
+        const int64_t row = r0 + (int64_t)run * a.Nout;
         for (int j = 0; j < nsl; ++j, ++js) {
           const int sl = js % kXtSlots;
           if (js >= kXtSlots && !ptx::mbar_wait(idx_empty(sl), ((js / kXtSlots) - 1) & 1, a.err)) {
@@ -346,20 +422,13 @@ __global__ void __launch_bounds__(kXtThreads, 1)
             break;
           }
           const int w = slice_width(j, G);
-          const uint32_t dst = base + kXtOffIdx + kXtIdxSlot * sl, bar = idx_full(sl);
-          const uint32_t per_row = (FMT == kFmtVq16 ? 2 * w : w + w / 2 * (kTwo ? 2 : 1)) + (block_scales ? w / 4 : 0);
-          ptx::mbar_arrive_expect_tx(bar, (uint32_t)(runs * nr) * per_row);
-          for (int h = 0; h < runs; ++h) {
-            const int64_t e = (int64_t)16 * j * N + (int64_t)(r0 + h * a.Nout) * w;  // entry of (slice j, first row)
-            const uint32_t o = 64u * h;                                             // first row in the slot
-            if (FMT == kFmtVq16) {
-              ptx::bulk_load(dst + o * w * 2, l.idx16 + e, nr * w * 2, bar);
-            } else {
-              ptx::bulk_load(dst + o * w, l.lo + e, nr * w, bar);
-              ptx::bulk_load(dst + kXtIdxHi + o * w / 2, l.hi4 + e / 2, nr * w / 2, bar);
-              if (kTwo) ptx::bulk_load(dst + kXtIdxS2 + o * w / 2, l.s2 + e / 2, nr * w / 2, bar);
-            }
-            if (block_scales) ptx::bulk_load(dst + kXtIdxSc + o * w / 4, l.scales + e / 8, nr * w / 4, bar);
+          const uint32_t bar = idx_full(sl);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(runs * nr) * all16 * (uint32_t)w / 16u);
+          __syncwarp();
+          if (mine && nr > 0) {
+            const int bytes = row16 * w / 16;  // of a row
+            ptx::bulk_load(base + kXtOffIdx + kXtIdxSlot * sl + off + (uint32_t)(64 * run * bytes),
+                           src + (int64_t)row16 * j * N + row * bytes, (uint32_t)(nr * bytes), bar);
           }
         }
       }
@@ -427,7 +496,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(acc_empty(b));
+      if (lane == 0) arrive_at(acc_empty(b), 0);
       return true;
     };
     for (int u = ubeg; ok && u < uend; ++u, ++ui) {
@@ -561,7 +630,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         ptx::tc_fence_before();
         if (!ok) break;
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(full_a(part));
+        if (lane == 0) arrive_at(full_a(part), 0);
         if (pending) {
           ok = finish_tile(prev, ui - 1);
           pending = false;
@@ -576,12 +645,13 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     if (!ok) *abort_flag = 1;
   }
 
-  // Every thread of the block gets here (all waits above are bounded).
+  // Every thread of both blocks gets here (all waits above are bounded).
   ptx::tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, tcols);
+    pair_tmem_dealloc(tmem, tcols);
   }
 }
 
@@ -609,9 +679,13 @@ static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, c
   if (!enc) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (a.rows) {  // x in row order
@@ -631,8 +705,8 @@ static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, c
   const cuuint64_t strides[1] = {(cuuint64_t)a.w.K * 2};
   const cuuint32_t estr[2] = {1, 1};
   for (int i = 0; i < kXtBoxes; ++i) {
-    const int rows = 64 << i;  // a tile of at most Tmax rows never takes a larger box than Tmax
-    const cuuint32_t box[2] = {64, (cuuint32_t)(rows < Tmax ? rows : Tmax)};
+    const int rows = 32 << i;  // half a tile of at most Tmax rows never takes a larger box than Tmax / 2
+    const cuuint32_t box[2] = {64, (cuuint32_t)(rows < Tmax / 2 ? rows : Tmax / 2)};
     if (enc(&maps.x[i], dt, 2, const_cast<uint16_t*>(a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -643,9 +717,10 @@ static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, c
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int nacc = 2 * ((Tmax + 31) / 32 * 32) + kXtParts * (int)kXtACols <= 512 ? 2 : 1;
-  cfg.gridDim = dim3(num_sms);
+  cfg.gridDim = dim3(num_sms / 2 * 2);
   cfg.blockDim = dim3(kXtThreads);
   cfg.dynamicSmemBytes = smem;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, maps, a, Tmax, nacc);
 }
 
