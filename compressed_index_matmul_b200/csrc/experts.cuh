@@ -110,26 +110,35 @@ __device__ __forceinline__ int expert_of(const ExpertTiles& t, int E, int u) {
   return lo;
 }
 
-// One group of a one- or two-stage format: w_j = RN_T(s c1_j + s c2_j) with the
-// mixed-precision fma (fp16 factors, fp32 sum): two operations a weight and no widening.
-// The scaled stage-2 half is rounded to fp32 before the sum, which is off by at most 2^-24 of
-// it; rounding the weight to T (2^-8 or 2^-11) is the MMA's operand type.
+// One group of a one- or two-stage format, with the rounding of the materialised weights
+// (vq_debug_dequant): w_j = RN_T(fl32(s * fl32(c1_j + c2_j))).  Forming s c1 + s c2 with
+// two mixed-precision multiply-adds a weight was no faster, and the sum in packed fp16 gained 2 %
+// for one rounding more: the decode waits for the shared-memory pipe (9 wavefronts a gather of 32
+// codewords, 4 for the shuffles), not for its arithmetic.
 template <typename T, bool kTwo>
 __device__ __forceinline__ void decode_scaled(const uint4& c1, const uint32_t (&c2)[4], unsigned short s,
                                               uint32_t* out) {
   const uint32_t w1[4] = {c1.x, c1.y, c1.z, c1.w};
+  const uint32_t sb = __float_as_uint(__half2float(__ushort_as_half(s)));
+  const uint64_t sv = (uint64_t)sb | ((uint64_t)sb << 32);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    float lo = -0.0f, hi = -0.0f;
-    if (kTwo)
-      asm("{ .reg .f16 l, h; mov.b32 {l, h}, %2; fma.rn.f32.f16 %0, l, %3, %4; fma.rn.f32.f16 %1, h, %3, %4; }"
+    float lo, hi;
+    if (kTwo) {
+      const float2 b = f16x2_to_f32x2(c2[q]);
+      asm("{ .reg .f16 l, h; mov.b32 {l, h}, %2; add.rn.f32.f16 %0, l, %3; add.rn.f32.f16 %1, h, %4; }"
           : "=f"(lo), "=f"(hi)
-          : "r"(c2[q]), "h"(s), "f"(-0.0f));
-    float a, b;
-    asm("{ .reg .f16 l, h; mov.b32 {l, h}, %2; fma.rn.f32.f16 %0, l, %3, %4; fma.rn.f32.f16 %1, h, %3, %5; }"
-        : "=f"(a), "=f"(b)
-        : "r"(w1[q]), "h"(s), "f"(lo), "f"(hi));
-    out[q] = Elt<T>::pack(a, b);
+          : "r"(w1[q]), "f"(b.x), "f"(b.y));
+    } else {
+      const float2 a = f16x2_to_f32x2(w1[q]);
+      lo = a.x;
+      hi = a.y;
+    }
+    uint64_t m;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(m)
+        : "l"((uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32)), "l"(sv));
+    out[q] = Elt<T>::pack(__uint_as_float((uint32_t)m), __uint_as_float((uint32_t)(m >> 32)));
   }
 }
 

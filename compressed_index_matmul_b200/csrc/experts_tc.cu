@@ -81,13 +81,6 @@ __global__ void __launch_bounds__(128) gather_rows_kernel(const uint4* __restric
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-  return p != 0;
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -119,23 +112,6 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
                "h"((unsigned short)3)
                : "memory");
-}
-
-// Lane-wise wait of a warp: every lane with `wait` polls its own barrier until all are through.
-__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, bool wait, volatile int* abort_flag,
-                                           uint32_t* err) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0; i < kWaitSpinLimit; ++i) {
-    const bool ok = !wait || ptx::mbar_try_wait(bar, parity);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    if ((i & 63u) == 63u) {
-      const uint64_t t = ptx::globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      if (__any_sync(0xffffffffu, *abort_flag || t - t0 > 1000000000ull)) break;
-    }
-  }
-  if (err && (threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
-  return false;
 }
 
 // One tile: its expert, its place, its x rows.
@@ -348,7 +324,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
           par = (uint32_t)((ui / nacc) - 1) & 1u;
           wait = true;
         }
-        if (!wait_lanes(bar, par, wait, abort_flag, a.err)) {
+        if (!ptx::mbar_wait_lanes(bar, par, wait, abort_flag, a.err)) {
           ok = false;
           break;
         }
@@ -356,7 +332,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         const uint32_t at = utmem + acol0 + kXtACols * st;
         const uint64_t b0 = ptx::smem_desc_sw128(b_tile(s, 0)), b1 = ptx::smem_desc_sw128(b_tile(s, 1));
         const bool two = slice_width(j, G) == 16;
-        if (elect_one()) {
+        if (ptx::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
             pair_umma_ts(acc, at + 8u * kk, b0 + 2u * kk, idesc, (j | kk) != 0);

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(tc_threads(kTcParts), kTcParts == 2 ? 2 : 1)
   const uint32_t b_bytes = (uint32_t)p.T * 128u;
   auto b_tile = [&](int s) { return base + kTcTilesOffset + b_bytes * s; };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int K = a.K, G = K / 8, N = a.N, M = a.M;
   const int row0 = blockIdx.x * kTcRows;
   const int rows_here = min(kTcRows, N - row0);
@@ -264,33 +264,39 @@ __global__ void __launch_bounds__(tc_threads(kTcParts), kTcParts == 2 ? 2 : 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kAbFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      const uint32_t idesc = ptx::idesc_f16(kAbFmt, kTcRows, (uint32_t)p.T);
-      bool ok = true;
-      int issued = 0;
-      for (int kb = 0; kb < nkb; ++kb) {
-        const int s = kb % kSt;
-        const uint32_t par = (kb / kSt) & 1;
-        if (*abort_flag || !ptx::mbar_wait(full_b(s), par, p.err) || !ptx::mbar_wait(full_a(s), par, p.err)) {
-          *abort_flag = 1;
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t at = tmem + acol0 + kTcACols * s;
-        const uint64_t bd = ptx::smem_desc_sw128(b_tile(s));
+    // The whole warp walks the blocks and one elected lane issues: with warp-uniform control flow
+    // the descriptors are in uniform registers, as tcgen05.mma takes them (issued from a loop of
+    // one lane, an MMA took 80 to 120 cycles).  Lane 0 polls the A stage's barrier and lane 1 the
+    // x stage's in one go: the decode's gathers keep the shared-memory pipe's queue long, and
+    // every poll waits in it.
+    constexpr uint32_t kAbFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    const uint32_t idesc = ptx::idesc_f16(kAbFmt, kTcRows, (uint32_t)p.T);
+    const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+    bool ok = true;
+    int issued = 0;
+    for (int kb = 0; kb < nkb; ++kb) {
+      const int s = kb % kSt;
+      if (!ptx::mbar_wait_lanes(lane == 0 ? full_a(s) : full_b(s), (kb / kSt) & 1, lane < 2, abort_flag, p.err)) {
+        *abort_flag = 1;
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t at = utmem + acol0 + kTcACols * s;
+      const uint64_t bd = ptx::smem_desc_sw128(b_tile(s));
+      if (ptx::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)  // A: +8 TMEM columns; B: +32 bytes along K inside the swizzle atom
-          ptx::umma_f16_ts(tmem, at + 8u * kk, bd + 2u * kk, idesc, (kb | kk) != 0);
+          ptx::umma_f16_ts(utmem, at + 8u * kk, bd + 2u * kk, idesc, (kb | kk) != 0);
         ptx::umma_commit(empty(s));
-        issued = kb + 1;
+        if (kb + 1 == nkb) ptx::umma_commit(accum_bar);
       }
-      ptx::umma_commit(accum_bar);
-      // On the abort path nobody else waits for the accumulator: drain the issued
-      // MMAs here before TMEM and shared memory are released.
-      if (!ok && issued) ptx::mbar_wait(accum_bar, 0, p.err);
+      __syncwarp();
+      issued = kb + 1;
     }
+    // On the abort path nobody else waits for the accumulator: drain the issued MMAs here before
+    // TMEM and shared memory are released.
+    if (!ok && issued) ptx::mbar_wait(empty((issued - 1) % kSt), ((issued - 1) / kSt) & 1, p.err);
   } else {
     // ------------------------------------------------------------ decode
     // Warp (quarter q, part) decodes every P-th k block, kb = part, part+P, ...: all

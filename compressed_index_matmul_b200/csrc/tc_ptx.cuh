@@ -59,6 +59,31 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
   return false;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+
+// Wait of a whole warp for several barriers in one poll: every lane with `wait` polls its own until
+// all are through.  The time limit of mbar_wait; also ends when *abort_flag is set.
+__device__ __forceinline__ bool mbar_wait_lanes(uint32_t bar, uint32_t parity, bool wait, volatile int* abort_flag,
+                                                uint32_t* err) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < kWaitSpinLimit; ++i) {
+    const bool ok = !wait || mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((i & 63u) == 63u) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (__any_sync(0xffffffffu, *abort_flag || t - t0 > 1000000000ull)) break;
+    }
+  }
+  if (err && (threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
+  return false;
+}
+
 // 1-D bulk copy global -> shared, completing `bytes` of transaction on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
