@@ -89,6 +89,8 @@ _lib = None
 def load(path: str | None = None):
     """Load libvqlinear.so and declare its signatures (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -27,14 +27,22 @@ struct ExpertsPlan {
   int Tmax;  // rows of a tile
 };
 
-// Rows per expert, were all T spread over as many experts as can have one, decide the
-// kernel: the counts themselves are on the device.
-ExpertsPlan plan_experts(const vq_experts_desc& d, int T, int forced) {
+// The kernel, from T, E and the layer (the row counts themselves are on the device): `busy`
+// experts can have rows, `avg` each.  The tensor-core kernel decodes 2.4 T weights a second whatever
+// the rows (to 256 of them), once its tiles of 256 rows of W fill the pairs of SMs; the warp-MMA kernel
+// 2.0 T at up to 16 rows, in tiles of 16 rows of W that fill the SMs earlier, and starts faster.
+// Measured, us, warp-MMA / tensor-core: 64 experts x 8 rows (2048 x 1024, 512 tiles) 81 / 57; 8 x 1
+// (2048 x 2048 gated, 64 tiles) 21.9 / 21.1; 8 x 2 (1024 x 576, 32 tiles) 9.4 / 13.1; 2 x 1 (2048 x
+// 2048 gated, 16 tiles) 11.4 / 19.9; 8 x 16 (2048 x 2048 gated) 25.0 / 21.0; 64 x 32 (2048 x 1024)
+// 179 / 57.
+ExpertsPlan plan_experts(const vq_experts_desc& d, int T, int forced, int num_sms) {
   const int busy = T < d.E ? T : d.E;
   const int avg = (T + busy - 1) / busy;
+  const int64_t tiles = (int64_t)busy * ((d.layer.N + 255) / 256);
   ExpertsPlan p{};
-  p.path = forced != VQ_PATH_AUTO ? forced : (avg <= 16 ? VQ_PATH_GEMV : VQ_PATH_TC);
-  p.Tmax = p.path == VQ_PATH_GEMV ? 16 : avg <= 32 ? 64 : avg <= 96 ? 128 : 256;
+  p.path = forced != VQ_PATH_AUTO ? forced : avg > 16 || 20 * tiles >= 8 * num_sms ? VQ_PATH_TC : VQ_PATH_GEMV;
+  // Tiles of up to 128 rows of x have a second accumulator; above, larger tiles save decodes.
+  p.Tmax = p.path == VQ_PATH_GEMV ? 16 : avg <= 64 ? 128 : 256;
   return p;
 }
 
@@ -109,7 +117,7 @@ VQ_API vq_status vq_experts_set_path(vq_experts_t h, int32_t path) {
 VQ_API vq_status vq_experts_plan(vq_experts_t h, int32_t T, vq_plan_info* out) {
   if (h == nullptr || out == nullptr) return fail(VQ_ERR_INVALID_ARG, "handle or out is NULL");
   if (T < 1 || T > h->d.layer.max_M) return fail(VQ_ERR_INVALID_ARG, "T=%d outside [1, max_M=%d]", T, h->d.layer.max_M);
-  const ExpertsPlan p = plan_experts(h->d, T, h->path);
+  const ExpertsPlan p = plan_experts(h->d, T, h->path, h->dev.num_sms);
   out->path = p.path;
   out->launches = p.path == VQ_PATH_TC && h->d.gather ? 2 : 1;
   out->ctas = h->dev.num_sms;
@@ -154,7 +162,7 @@ VQ_API vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_row
   a.act = h->d.act;
   a.glu = h->d.glu;
   a.shared = h->d.shared_codebooks;
-  const ExpertsPlan p = plan_experts(h->d, T, h->path);
+  const ExpertsPlan p = plan_experts(h->d, T, h->path, h->dev.num_sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = p.path == VQ_PATH_TC ? launch_experts_tc(a, h->xs, p.Tmax, h->dev.num_sms, s)
                                        : launch_experts_gemv(a, h->dev.num_sms, s);

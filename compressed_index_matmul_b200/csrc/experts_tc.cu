@@ -53,7 +53,7 @@ constexpr uint32_t kXtOffTiles = 65536;                // after the codebook
 constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 16;
 constexpr uint32_t kXtOffIdx = kXtOffBars + 768;
 constexpr uint32_t kXtOffX = (kXtOffIdx + kXtSlots * kXtIdxSlot + 1023) / 1024 * 1024;
-// Tmax is 64, 128 or 256 (the boxes' heights).
+// Tmax is 128 or 256 (twice the heights of the larger boxes).
 // At least 144 KiB, so that no other kernel of this library that allocates TMEM (94 KiB and more a
 // block) shares the SM: a pair takes all 512 columns of both SMs, and two pairs that each hold one
 // SM's TMEM and wait for the other's would never go on.

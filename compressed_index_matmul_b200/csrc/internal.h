@@ -83,6 +83,8 @@ cudaError_t launch_lut(const LayerArgs& a, const Plan& p, float* scratch, uint32
 cudaError_t launch_vq16(const LayerArgs& a, const Plan& p, const int8_t* signs, cudaStream_t s);
 cudaError_t launch_tc(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* tickets, uint32_t* err_flag,
                       cudaStream_t s);
+cudaError_t launch_tc_fused(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* tickets, uint32_t* err_flag,
+                            cudaStream_t s);  // launch_tc's, with a.epi
 cudaError_t launch_split_reduce(const float* partial, void* y, int splits, int M, int N, int act, cudaStream_t s);
 cudaError_t launch_rht(const void* x, void* x_out, const int8_t* signs, int M, int K, int dtype,
                        cudaStream_t s);

@@ -27,7 +27,7 @@ def _raw_stream(stream, index):
 
 def check_tensor(t, name, shape, dtype, device):
     """Raise ValueError unless `t` is a contiguous tensor of this shape, type and device."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}: got "
                          f"{t.dtype} {list(t.shape)} on {t.device}, strides {list(t.stride())}")
 

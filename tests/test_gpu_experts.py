@@ -332,11 +332,12 @@ def test_planes_past_32_bits(path):
         big[k][E - 1] = src[0].cuda()
     assert (E - 1) * n > 2 ** 32
     X = vq.VQExperts(E, N, K, FMT_RVQ12_4, 64, DT_BF16, 20, big, shared_codebooks=True)
-    Y = vq.VQExperts(1, N, K, FMT_RVQ12_4, 64, DT_BF16, 20, arrays)
+    eight = {k: v if k in ("cb1", "cb2") else np.concatenate([v] * 8) for k, v in arrays.items()}
+    Y = vq.VQExperts(8, N, K, FMT_RVQ12_4, 64, DT_BF16, 20, eight, shared_codebooks=True)
     X.set_path(path)
     Y.set_path(path)
     x = randn((20, K), DT_BF16, 7)
-    assert torch.equal(X.forward(x, offsets_of([0] * (E - 1) + [20])), Y.forward(x, offsets_of([20])))
+    assert torch.equal(X.forward(x, offsets_of([0] * (E - 1) + [20])), Y.forward(x, offsets_of([0] * 7 + [20])))
 
 
 @pytest.mark.parametrize("tokens", [1, 5, 200])
