@@ -28,19 +28,19 @@ struct ExpertsPlan {
 };
 
 // The kernel, from T, E and the layer (the row counts themselves are on the device): `busy`
-// experts can have rows, `avg` each.  The tensor-core kernel decodes 2.4 T weights a second whatever
-// the rows (to 256 of them), once its tiles of 256 rows of W fill the pairs of SMs; the warp-MMA kernel
-// 2.0 T at up to 16 rows, in tiles of 16 rows of W that fill the SMs earlier, and starts faster.
-// Measured, us, warp-MMA / tensor-core: 64 experts x 8 rows (2048 x 1024, 512 tiles) 81 / 57; 8 x 1
-// (2048 x 2048 gated, 64 tiles) 21.9 / 21.1; 8 x 2 (1024 x 576, 32 tiles) 9.4 / 13.1; 2 x 1 (2048 x
-// 2048 gated, 16 tiles) 11.4 / 19.9; 8 x 16 (2048 x 2048 gated) 25.0 / 21.0; 64 x 32 (2048 x 1024)
-// 179 / 57.
+// experts can have rows, `avg` each.  The tensor-core kernel decodes 2.4 T weights a second for up to
+// 256 rows, once its tiles of 256 rows of W fill the SMs; the warp-MMA kernel as many for up to 8, and
+// again for every 16 rows that an expert has, in tiles of 16 rows of W that fill the SMs sooner, and
+// it starts faster.  Measured, us, warp-MMA / tensor-core: 64 experts x 1 row (2048 x 1024, 512
+// tiles) 54 / 56, x 8 (up to 18) 74 / 56, x 32 179 / 57; 8 x 1 (2048 x 2048 gated, 64 tiles) 18.0 /
+// 20.7, x 16 21.3 / 20.8; 8 x 2 (1024 x 576, 32 tiles) 8.5 / 13.0; 2 x 1 (2048 x 2048 gated, 16
+// tiles) 9.4 / 19.6; 16-bit indices, 16 x 12 (1536 x 576, 96 tiles) 19.4 / 21.8, x 25 27.5 / 22.7.
 ExpertsPlan plan_experts(const vq_experts_desc& d, int T, int forced, int num_sms) {
   const int busy = T < d.E ? T : d.E;
   const int avg = (T + busy - 1) / busy;
   const int64_t tiles = (int64_t)busy * ((d.layer.N + 255) / 256);
   ExpertsPlan p{};
-  p.path = forced != VQ_PATH_AUTO ? forced : avg > 16 || 20 * tiles >= 8 * num_sms ? VQ_PATH_TC : VQ_PATH_GEMV;
+  p.path = forced != VQ_PATH_AUTO ? forced : avg <= 2 || (avg <= 14 && tiles < num_sms) ? VQ_PATH_GEMV : VQ_PATH_TC;
   // Tiles of up to 128 rows of x have a second accumulator; above, larger tiles save decodes.
   p.Tmax = p.path == VQ_PATH_GEMV ? 16 : avg <= 64 ? 128 : 256;
   return p;
@@ -62,6 +62,8 @@ vq_status validate_experts(const vq_experts_desc* d) {
     return fail(VQ_ERR_UNSUPPORTED, "rht and corr must be 0: rotate x with vq_rht_apply; experts carry no correction");
   if (d->layer.N % (d->glu ? 16 : 8) != 0)
     return fail(VQ_ERR_UNSUPPORTED, "N=%d must be a multiple of %d", d->layer.N, d->glu ? 16 : 8);
+  if ((int64_t)d->layer.N * (d->layer.K / 8) > INT32_MAX)
+    return fail(VQ_ERR_UNSUPPORTED, "N=%d x K=%d: an expert may have at most 2^31 - 1 groups", d->layer.N, d->layer.K);
   // the tiles of a call are counted in 32 bits: at most 8 outputs by 16 rows each
   const int64_t rt = (d->layer.N / (d->glu ? 2 : 1) + 7) / 8;
   if (rt * ((int64_t)d->layer.max_M / 16 + d->E) > INT32_MAX)

@@ -179,12 +179,10 @@ class VQRouter:
             raise ValueError(f"logits must be float16, bfloat16 or float32: got {logits.dtype}")
         check_tensor(logits, "logits", (T, E), logits.dtype, dev)
         if out is None:
-            # one allocation, each part 16-byte aligned
-            n = T * k
-            pad, po = -n % 4, -(E + 1) % 4
-            buf = torch.empty(4 * (n + pad) + E + 1 + po, dtype=torch.int32, device=dev)
-            ids, _, w, _, rows, _, slots, _, offsets, _ = buf.split_with_sizes((n, pad, n, pad, n, pad, n, pad, E + 1, po))
-            out = VQRouting(ids.view(T, k), w.view(torch.float32).view(T, k), offsets, rows, slots.view(T, k))
+            i32 = torch.int32
+            out = VQRouting(torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), device=dev, dtype=torch.float32),
+                            torch.empty(E + 1, dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev),
+                            torch.empty((T, k), dtype=i32, device=dev))
         else:
             for name, shape, dt in (("ids", (T, k), torch.int32), ("weights", (T, k), torch.float32),
                                     ("offsets", (E + 1,), torch.int32), ("rows", (T * k,), torch.int32),

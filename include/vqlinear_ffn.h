@@ -109,8 +109,9 @@ vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_rows, cons
 /* The kernel of later forwards: VQ_PATH_GEMV (warp MMAs on weights decoded in registers;
  * tiles of 16 rows of W by up to 16 rows of an expert), VQ_PATH_TC (tcgen05 on weights decoded
  * into tensor memory; tiles of 256 rows of W by up to 256), or VQ_PATH_AUTO, which goes by T, E and
- * the layer's shape: VQ_PATH_GEMV while T rows spread over min(E, T) experts come to at most 16
- * each and the larger tiles would leave most SMs idle (the counts themselves stay on the device). */
+ * the layer's shape: VQ_PATH_GEMV while T rows spread over min(E, T) experts come to at most 2
+ * each, or 14 where the larger tiles are fewer than the SMs (the counts themselves stay on the
+ * device). */
 vq_status vq_experts_set_path(vq_experts_t h, int32_t path);
 
 /* As vq_linear_plan, for a forward of T rows (launches: with rows, if desc.gather == 1). */

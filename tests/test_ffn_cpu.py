@@ -136,7 +136,7 @@ def test_combine_checks_its_tensors():
 @pytest.mark.parametrize("kw,status", [
     (dict(E=0), 1), (dict(E=1025), 2), (dict(gather=2), 1), (dict(glu=2), 1), (dict(act=5), 1), (dict(act=-1), 1), (dict(shared_codebooks=3), 1),
     (dict(N=12), 2), (dict(N=72, glu=1), 2), (dict(K=72), 1), (dict(K=80), 2), (dict(fmt=9), 1), (dict(max_rows=0), 1),
-    (dict(rht=1), 2), (dict(corr=1), 2), (dict(N=1 << 24, max_rows=1 << 20, E=1024), 2),
+    (dict(rht=1), 2), (dict(corr=1), 2), (dict(N=1 << 17, K=1 << 17), 2), (dict(N=1 << 24, max_rows=1 << 20, E=1024), 2),
     (dict(fmt=B.VQ_FMT_VQ16_RVQ, n16=5), 1),
 ])
 def test_experts_reject_bad_descriptors(lib, kw, status):

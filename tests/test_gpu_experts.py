@@ -173,7 +173,7 @@ def test_many_experts_with_few_rows(oracle, path):
 def test_automatic_choice(oracle):
     for counts in ([1] * 4, [100, 200, 3, 0]):
         X, *_ = run(oracle, 4, 128, 256, FMT_RVQ12_4, 64, DT_BF16, counts, vq.VQ_PATH_AUTO)
-    assert X.plan(1)["path"] == GEMV and X.plan(64)["path"] == GEMV and X.plan(303)["path"] == TC
+    assert X.plan(1)["path"] == GEMV and X.plan(56)["path"] == GEMV and X.plan(57)["path"] == TC and X.plan(303)["path"] == TC
 
 
 @pytest.mark.parametrize("path", [GEMV, TC])
