@@ -138,6 +138,13 @@ vq_status check_current_device(int device) {
   return VQ_OK;
 }
 
+// Test hook: VQ_TEST_FAIL_ALLOC=1 makes the device allocations fail, so callers'
+// handling of VQ_ERR_NOMEM can be tested without exhausting a shared GPU.
+vq_status refuse_alloc() {
+  const char* v = getenv("VQ_TEST_FAIL_ALLOC");
+  return v && v[0] == '1' ? fail(VQ_ERR_NOMEM, "device allocation refused (VQ_TEST_FAIL_ALLOC=1)") : VQ_OK;
+}
+
 static vq_status check_device(const vq_linear_s* h) { return check_current_device(h->dev.device); }
 
 vq_status query_device(DeviceInfo* dev) {
@@ -270,11 +277,7 @@ VQ_API vq_status vq_linear_create(const vq_linear_desc* desc, vq_linear_t* out) 
       if (p.sync_words > sync_words) sync_words = p.sync_words;
     }
   }
-  // Test hook: VQ_TEST_FAIL_ALLOC=1 makes the device allocations fail, so callers'
-  // handling of VQ_ERR_NOMEM can be tested without exhausting a shared GPU.
-  const char* fail_alloc = getenv("VQ_TEST_FAIL_ALLOC");
-  if (fail_alloc && fail_alloc[0] == '1')
-    return fail(VQ_ERR_NOMEM, "device allocation refused (VQ_TEST_FAIL_ALLOC=1)");
+  if ((st = refuse_alloc())) return st;
   vq_linear_s* h = new (std::nothrow) vq_linear_s{};
   if (!h) return fail(VQ_ERR_NOMEM, "host allocation of the handle failed");
   h->d = *desc;

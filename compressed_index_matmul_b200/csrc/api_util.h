@@ -22,6 +22,8 @@ LayerArgs make_args(const vq_linear_desc& d, const vq_planes* p, const vq_codebo
 // The current device, which must be sm_100.
 vq_status query_device(DeviceInfo* dev);
 vq_status check_current_device(int device);
+// VQ_ERR_NOMEM where the test hook VQ_TEST_FAIL_ALLOC=1 is set.
+vq_status refuse_alloc();
 // Waits for all work of `device` and frees a and b (either may be NULL) there.
 cudaError_t free_on_device(int device, void* a, void* b = nullptr);
 // Whether the byte ranges [a, a + na) and [b, b + nb) meet.

@@ -10,7 +10,8 @@
 // negative v, where 1 + tanh(u) cancels.  The erf form is v/2 * erfc(-v / sqrt 2) for the
 // same reason.  The exponential and the quotient are the fast ones (__expf, __fdividef): off by
 // a few units of 2^-24 relative, plus |u| of them for the exponential's argument, where
-// the store rounds to 2^-11 or 2^-8.
+// the store rounds to 2^-11 or 2^-8; a quotient by more than 2^126 is 0, so an activation below
+// |v| 2^-126 is.
 #pragma once
 
 #include "common.cuh"

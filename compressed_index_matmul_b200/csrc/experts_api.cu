@@ -80,6 +80,7 @@ VQ_API vq_status vq_experts_create(const vq_experts_desc* desc, vq_experts_t* ou
   if (st) return st;
   DeviceInfo dev{};
   if ((st = query_device(&dev))) return st;
+  if ((st = refuse_alloc())) return st;
   vq_experts_s* h = new (std::nothrow) vq_experts_s{};
   if (!h) return fail(VQ_ERR_NOMEM, "host allocation of the handle failed");
   h->d = *desc;
@@ -122,7 +123,7 @@ VQ_API vq_status vq_experts_plan(vq_experts_t h, int32_t T, vq_plan_info* out) {
   const ExpertsPlan p = plan_experts(h->d, T, h->path, h->dev.num_sms);
   out->path = p.path;
   out->launches = p.path == VQ_PATH_TC && h->d.gather ? 2 : 1;
-  out->ctas = h->dev.num_sms;
+  out->ctas = p.path == VQ_PATH_TC ? h->dev.num_sms / 2 * 2 : h->dev.num_sms;
   out->splits = 1;
   return VQ_OK;
 }

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kXgThreads, 1) experts_gemv_kernel(const __gri
   };
 
   // The load stream runs one slice ahead of the decode: tile lu of expert le, slice ls.
-  int lu = ubeg + grp, le = e_first, ls = kp, lrt = 0, ltk = 0;
+  int lu = ubeg + grp, le = e_first, ls = kp, lrt = 0, ltk = 0;  // kp < nsl: a group has at most nsl warps
   uint32_t lq = 0;         // entry of (slice ls, row 0)
   int rA = 0, rB = 0;      // the lane's two rows of W; past the last one they repeat it (not stored)
   LayerArgs lw = expert_layer(a, le);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kXgThreads, 1) experts_gemv_kernel(const __gri
   bool more = lu < uend;
   if (more) {
     load_tile();
-    if (kp < nsl) load_slice(iq);
+    load_slice(iq);
   }
   int tok_e = -1, tok_tk = -1, nt = 1;
   const uint16_t* xp[2] = {a.x, a.x};
@@ -351,17 +351,13 @@ __global__ void __launch_bounds__(kXgThreads, 1) experts_gemv_kernel(const __gri
     };
     for (int s = kp; s < nsl; s += wk) {
       more = advance();
-      if (more && kp < nsl) load_slice(nq);
+      if (more) load_slice(nq);
       if (nt == 1)
         slice(std::integral_constant<int, 1>{}, s);
       else
         slice(std::integral_constant<int, 2>{}, s);
       iq[0] = nq[0];
       iq[1] = nq[1];
-    }
-    if (kp >= nsl) {  // fewer slices than warps: this one only follows the tiles
-      ls = nsl;
-      more = advance();
     }
 
     if (bad) {
@@ -436,8 +432,9 @@ __global__ void __launch_bounds__(kXgThreads, 1) experts_gemv_kernel(const __gri
 
 // Warps per tile: as many as give every warp of the device a share of the tiles of eight experts
 // (a token's, say; or of all, where there are fewer), at most one per slice of K.  It goes by the
-// layer and E alone, so that a row's sum is taken in the same order whatever the call's other rows.  At 8 rows for 8 experts, us: 2048 x 2048
-// 20.7 with 2 warps, 21.5 with 4, 24.1 with 1 (no sums to exchange, but 14 % of the warps idle).
+// layer and E alone, so that a row's sum is taken in the same order whatever the call's other rows.
+// At 8 rows for 8 experts of 2048 x 2048, us: 20.7 with 2 warps, 21.5 with 4, 24.1 with 1 (no sums to
+// exchange, but 14 % of the warps idle).
 static int xg_wk(int E, int N, int K, int num_sms) {
   const int nsl = (K + 127) / 128, tiles = (E < 8 ? E : 8) * ((N + 15) / 16);
   int wk = 16;

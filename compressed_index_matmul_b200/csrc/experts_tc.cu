@@ -7,17 +7,18 @@
 // tcgen05.mma.cta_group::2 multiplies both, so an SM reads half of the x that a tile of its
 // own would need (with tiles per block the x loads, 32 KiB per 64 inputs and SM, ran at the
 // L2's 7 TB/s and set the pace).  The tiles of all experts are numbered in expert order
-// (find_tiles) and cut into one contiguous, equal range per pair, so a pair changes its
+// (find_tiles) and cut into one contiguous range of equal cost per pair, so a pair changes its
 // expert, and with it the codebook in shared memory, once or twice.
-//   warp 0     lane 0: x, per 64-wide k block, TMA loads of the block's half of the tile's x rows (32
-//              rows a copy, 128-byte swizzle) into a ring of S stages
-//   warp 1     allocates TMEM; lane 0 of the first block issues tcgen05.mma (M = 256, N = the
-//              tile's rows rounded up to 16, K = 16), A from both blocks' TMEM, B from both
-//              blocks' shared memory, and commits each stage to both; lane 0 of the second passes
+//   warp 0     lane 0: x, per 128-input slice, a TMA load per 64 inputs of the block's half of the
+//              tile's x rows (a box of 32, 64 or 128 rows, 128-byte swizzle: one large load
+//              instead of several small ones) into a ring of four stages
+//   warp 1     allocates TMEM; in the first block an elected lane issues tcgen05.mma (M = 256, N =
+//              the tile's rows rounded up to 16, K = 16), A from both blocks' TMEM, B from both
+//              blocks' shared memory, and commits each stage to both; the second block's passes
 //              its x stages' arrivals on
 //   warp 2     the expert's 12-bit codebook (one bulk copy when it changes) and, per
 //              128-input slice, the index bytes of the block's rows (one contiguous run per
-//              plane; glu: two) into a ring of slots
+//              plane; glu: two; a lane each) into a ring of four slots
 //   warps 4..  decode: four per TMEM lane quarter; thread = one row of W (its lane).
 //              Slice `js` of the pair's whole sequence goes to warp js % 4 of every quarter, into A
 //              stage js % 4 (64 TMEM columns, 128 inputs).  After a tile's last slice the same

@@ -32,6 +32,7 @@ constexpr int kRouteMaxE = 512;
 constexpr int kRouteMaxK = 32;
 constexpr int kRouteTile = 64;    // tokens ranked together: four per warp
 constexpr int kRouteBlocks = 128; // blocks of the two-kernel form, at most
+constexpr int kRouteMaxT = 1 << 30; // token numbers, rounded up to whole tiles, stay 32-bit
 
 struct RouteArgs {
   const void* logits;
@@ -424,11 +425,12 @@ VQ_API vq_status vq_router_create(const vq_router_desc* desc, vq_router_t* out) 
     return fail(VQ_ERR_UNSUPPORTED, "E=%d, k=%d: at most %d experts and %d choices", desc->E, desc->k, kRouteMaxE,
                 kRouteMaxK);
   if (desc->renorm != 0 && desc->renorm != 1) return fail(VQ_ERR_INVALID_ARG, "renorm=%d must be 0 or 1", desc->renorm);
-  if (desc->max_T < 1 || (int64_t)desc->max_T * desc->k > INT32_MAX)
-    return fail(VQ_ERR_INVALID_ARG, "max_T=%d: need max_T >= 1 and max_T * k < 2^31", desc->max_T);
+  if (desc->max_T < 1 || desc->max_T > kRouteMaxT || (int64_t)desc->max_T * desc->k > INT32_MAX)
+    return fail(VQ_ERR_INVALID_ARG, "max_T=%d: need 1 <= max_T <= 2^30 and max_T * k < 2^31", desc->max_T);
   DeviceInfo dev{};
   vq_status st = query_device(&dev);
   if (st) return st;
+  if ((st = refuse_alloc())) return st;
   vq_router_s* h = new (std::nothrow) vq_router_s{};
   if (!h) return fail(VQ_ERR_NOMEM, "host allocation of the handle failed");
   h->d = *desc;
@@ -466,6 +468,20 @@ VQ_API vq_status vq_router_forward(vq_router_t h, const void* logits, int32_t dt
   if (T > 0 && ((st = check_ptr(logits, "logits")) || (st = check_ptr(ids, "ids")) || (st = check_ptr(weights, "weights")) ||
                 (st = check_ptr(rows, "rows")) || (st = check_ptr(slots, "slots"))))
     return st;
+  if (T > 0) {
+    const size_t pairs = (size_t)T * d.k * 4;
+    const struct {
+      const void* p;
+      size_t bytes;
+      const char* name;
+    } bufs[6] = {{logits, (size_t)T * d.E * (dtype == VQ_F32 ? 4 : 2), "logits"}, {ids, pairs, "ids"},
+                 {weights, pairs, "weights"}, {offsets, sizeof(int32_t) * (d.E + 1), "offsets"}, {rows, pairs, "rows"},
+                 {slots, pairs, "slots"}};
+    for (int i = 0; i < 6; ++i)
+      for (int j = 0; j < i; ++j)
+        if (overlaps(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
+          return fail(VQ_ERR_INVALID_ARG, "%s overlaps %s", bufs[i].name, bufs[j].name);
+  }
   if ((st = check_current_device(h->device))) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;

@@ -371,7 +371,8 @@ vq_status vq_debug_dequant(vq_linear_t h, const vq_planes* planes, const vq_code
  * handle's error flag and ends normally (nothing faults, the context stays
  * usable); vq_linear_check then returns VQ_ERR_TIMEOUT and clears the flag.
  * The test hook for allocation failures is the environment variable
- * VQ_TEST_FAIL_ALLOC=1, which makes vq_linear_create return VQ_ERR_NOMEM. */
+ * VQ_TEST_FAIL_ALLOC=1, which makes vq_linear_create (and the
+ * creates of vqlinear_ffn.h) return VQ_ERR_NOMEM. */
 vq_status vq_debug_wait_timeout(vq_linear_t h, void* stream);
 
 #ifdef __cplusplus

@@ -126,7 +126,7 @@ typedef struct {
   int32_t E;      /* experts, 1 .. 512 */
   int32_t k;      /* experts per token, 1 .. min(E, 32) */
   int32_t renorm; /* 1: a token's k weights add up to 1; 0: they are softmax probabilities over all E */
-  int32_t max_T;  /* largest token count of a call; max_T * k < 2^31 */
+  int32_t max_T;  /* largest token count of a call, 1 .. 2^30; max_T * k < 2^31 */
 } vq_router_desc;
 
 typedef struct vq_router_s* vq_router_t;
@@ -152,13 +152,14 @@ vq_status vq_router_destroy(vq_router_t h);
  * for them; offsets[E] counts the pairs there are, and rows from offsets[E] on is left
  * as it was.
  *   logits   [T][E], VQ_F16, VQ_BF16 or VQ_F32 (`dtype`)
+ * logits and the five outputs must not overlap one another.
  * One kernel for small T, else two, on `stream`.  T == 0 writes zero offsets. */
 vq_status vq_router_forward(vq_router_t h, const void* logits, int32_t dtype, int32_t* ids, float* weights,
                             int32_t* offsets, int32_t* rows, int32_t* slots, int32_t T, void* stream);
 
 /* out[t] = RN(sum_j weights[t][j] * y[slots[t][j]] + residual[t]): the experts' rows back to
  * their tokens, summed in fp32 in the order of j, one rounding.
- *   y         [y_rows][N], VQ_F16 or VQ_BF16 (`dtype`); N % 8 == 0, else VQ_ERR_UNSUPPORTED
+ *   y         [y_rows][N], VQ_F16 or VQ_BF16 (`dtype`); N % 8 == 0 and N <= 2^24, else VQ_ERR_UNSUPPORTED
  *   weights   fp32 [T][k];  slots  int32 [T][k]; a slot outside [0, y_rows) contributes
  *             nothing (its weight is not used)
  *   residual  [T][N] or NULL; may be `out`

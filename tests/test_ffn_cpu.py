@@ -87,6 +87,7 @@ def test_fused_forward_checks_its_tensors_before_the_library():
 @pytest.mark.parametrize("E,k,max_T,renorm,status", [
     (0, 1, 1, 0, 1), (4, 0, 1, 0, 1), (4, 5, 1, 0, 1), (513, 1, 1, 0, 2), (64, 33, 1, 0, 2), (4, 1, 0, 0, 1),
     (4, 1, 1, 2, 1), (64, 32, 1 << 26, 0, 1),
+    (1, 1, (1 << 30) + 1, 0, 1),
 ])
 def test_router_rejects_bad_descriptors(lib, E, k, max_T, renorm, status):
     h = ctypes.c_void_p(1)

@@ -173,6 +173,17 @@ def test_router_refusals():
         R.forward(torch.zeros((4, 16), device="cuda"), out=R.forward(torch.zeros((5, 16), device="cuda")))
     with pytest.raises(vq.VQError, match="16-byte"):
         R.forward(torch.zeros(4 * 16 + 1, device="cuda")[1:].view(4, 16))
+    r = R.forward(torch.zeros((4, 16), device="cuda"))
+    logits = torch.zeros((4, 16), device="cuda")
+    for out, names in ((r._replace(slots=r.ids), "slots overlaps ids"), (r._replace(rows=r.ids.view(-1)), "rows overlaps ids"),
+                       (r._replace(weights=logits.view(-1)[8:16].view(4, 2)), "weights overlaps logits")):
+        with pytest.raises(vq.VQError, match=names):
+            R.forward(logits, out=out)
+
+
+def test_no_tokens():
+    r = vq.VQRouter(16, 2, 8).forward(torch.zeros((0, 16), device="cuda"))
+    assert r.ids.shape == (0, 2) and r.rows.shape == (0,) and r.offsets.tolist() == [0] * 17
 
 
 # ------------------------------------------------------------------------------------ combine
