@@ -25,6 +25,17 @@ def _raw_stream(stream, index):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream=None):
+    """An uninitialised tensor for work on `stream` (None: the device's current stream), taken from
+    that stream's memory: a block freed on another one may still be in use there."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_raw_stream(stream, device.index), device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def check_tensor(t, name, shape, dtype, device):
     """Raise ValueError unless `t` is a contiguous tensor of this shape, type and device."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
@@ -129,7 +140,7 @@ class VQLinear:
         if signs is not None:
             check_tensor(signs, "signs", (self.K,), torch.int8, dev)
         if y is None:
-            y = torch.empty((M, N), dtype=dt, device=dev)
+            y = _new((M, N), dt, dev, stream)
         else:
             check_tensor(y, "y", (M, N), dt, dev)
         if M > 0:

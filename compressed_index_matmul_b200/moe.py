@@ -6,7 +6,7 @@ from __future__ import annotations
 from typing import TYPE_CHECKING, NamedTuple
 
 from . import _binding as B
-from .layer import _raw_stream, check_tensor
+from .layer import _new, _raw_stream, check_tensor
 
 if TYPE_CHECKING:
     import torch
@@ -109,7 +109,7 @@ class VQExperts:
             T = rows.shape[0]
             check_tensor(rows, "rows", (T,), torch.int32, dev)
         if y is None:
-            y = torch.empty((T, self.n_out), dtype=dt, device=dev)
+            y = _new((T, self.n_out), dt, dev, stream)
         else:
             check_tensor(y, "y", (T, self.n_out), dt, dev)
         if T > 0:
@@ -180,9 +180,8 @@ class VQRouter:
         check_tensor(logits, "logits", (T, E), logits.dtype, dev)
         if out is None:
             i32 = torch.int32
-            out = VQRouting(torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), device=dev, dtype=torch.float32),
-                            torch.empty(E + 1, dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev),
-                            torch.empty((T, k), dtype=i32, device=dev))
+            out = VQRouting(_new((T, k), i32, dev, stream), _new((T, k), torch.float32, dev, stream),
+                            _new(E + 1, i32, dev, stream), _new(T * k, i32, dev, stream), _new((T, k), i32, dev, stream))
         else:
             for name, shape, dt in (("ids", (T, k), torch.int32), ("weights", (T, k), torch.float32),
                                     ("offsets", (E + 1,), torch.int32), ("rows", (T * k,), torch.int32),
@@ -224,7 +223,7 @@ def combine(y, weights, slots, residual=None, out=None, stream=None):
     if residual is not None:
         check_tensor(residual, "residual", (T, N), y.dtype, dev)
     if out is None:
-        out = torch.empty((T, N), dtype=y.dtype, device=dev)
+        out = _new((T, N), y.dtype, dev, stream)
     else:
         check_tensor(out, "out", (T, N), y.dtype, dev)
     B.vq_experts_combine(y, n, weights, slots, residual, out, T, k, N,

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import compressed_index_matmul_b200 as vq
+from compressed_index_matmul_b200 import _binding as B
 from synth import DT_BF16, DT_F16, FMT_RVQ12, FMT_RVQ12_4, FMT_VQ16, FMT_VQ16_RVQ, LayerSpec, make_layer
 from tests.ffn_util import ACTS, epilogue64, epilogue_bound, glu64, glu_bound, product_bound
 from tests.gpu_util import require_gpu
@@ -416,3 +417,36 @@ def test_refusals():
         vq.VQExperts(E, N, K, FMT_RVQ12_4, 64, DT_BF16, T, arrays, bias=torch.zeros(N, device="cuda"))
     torch.cuda.synchronize()
     vq.vq_experts_check(X.handle)
+
+
+def test_allocation_failure(monkeypatch):
+    monkeypatch.setenv("VQ_TEST_FAIL_ALLOC", "1")
+    with pytest.raises(vq.VQError) as ei:
+        vq.vq_experts_create(2, 64, 128, FMT_RVQ12_4, 64, DT_BF16, 16)
+    assert ei.value.status == B.VQ_ERR_NOMEM
+    with pytest.raises(vq.VQError) as ei:
+        vq.vq_router_create(8, 2, 16)
+    assert ei.value.status == B.VQ_ERR_NOMEM
+    monkeypatch.delenv("VQ_TEST_FAIL_ALLOC")
+    vq.vq_router_destroy(vq.vq_router_create(8, 2, 16))
+
+
+def test_results_come_from_the_memory_of_the_given_stream():
+    """A result for another stream is not put where the current stream's freed blocks are: work on
+    the current stream may still use those."""
+    E, N, K, T = 2, 64, 128, 16
+    _, arrays = make_experts(E, N, K, FMT_RVQ12_4, 64, 21)
+    X = vq.VQExperts(E, N, K, FMT_RVQ12_4, 64, DT_BF16, T, arrays)
+    L = vq.VQLinear(N, K, FMT_RVQ12_4, 64, DT_BF16, T, {k: v[0] for k, v in arrays.items()})
+    R = vq.VQRouter(E, 1, T)
+    x, off, logits = randn((T, K), DT_BF16, 1), offsets_of([8, 8]), torch.zeros((T, E), device="cuda")
+    r, side = R.forward(logits), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda s: X.forward(x, off, stream=s), lambda s: L.forward_fused(x, stream=s),
+                 lambda s: R.forward(logits, stream=s).weights, lambda s: vq.combine(x, r.weights, r.slots, stream=s)):
+        here = call(None)
+        at = here.data_ptr()
+        del here
+        for s in (side, side.cuda_stream):
+            assert call(s).data_ptr() != at
+    torch.cuda.synchronize()
