@@ -30,7 +30,8 @@ constexpr int kRouteWarps = 16;
 constexpr int kRouteThreads = 32 * kRouteWarps;
 constexpr int kRouteMaxE = 512;
 constexpr int kRouteMaxK = 32;
-constexpr int kRouteTile = 64;    // tokens ranked together: four per warp
+constexpr int kRoutePer = 4;      // tokens of a warp that are chosen and ranked together
+constexpr int kRouteTile = kRoutePer * kRouteWarps;
 constexpr int kRouteBlocks = 128; // blocks of the two-kernel form, at most
 constexpr int kRouteMaxT = 1 << 30; // token numbers, rounded up to whole tiles, stay 32-bit
 
@@ -75,59 +76,85 @@ __device__ __forceinline__ void load_keys(const RouteArgs& a, int t, int lane, u
   for (int i = 0; i < EPL; ++i) key[i] = order_key(v[i] + 0.f);  // -0 and +0 are equal logits: one key
 }
 
-// The choices of a token by one warp, from its keys: lane j < k ends with choice j
-// (expert or -1) and its weight.
-template <int EPL>
-__device__ __forceinline__ void choose(const RouteArgs& a, uint32_t (&key)[EPL], int lane, int& id, float& w) {
-  uint32_t best = 0u;
+// The choices of P tokens by one warp, from their keys: lane j < k ends with choice j of token
+// q (expert or -1) and its weight.  The tokens' chains of reductions are independent, so a warp
+// that has several of them waits for one latency instead of P.
+template <int EPL, int P>
+__device__ __forceinline__ void choose(const RouteArgs& a, uint32_t (&key)[P][EPL], int lane, int (&id)[P],
+                                       float (&w)[P]) {
+  uint32_t best[P], m[P], top[P], mine[P];  // this lane's largest key, the warp's, the token's, the chosen one's
+  float all[P];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) best = max(best, key[i]);
-  id = -1;
-  uint32_t mine = 0u;
-  uint32_t top = 0u;
-  float all = 0.f;
+  for (int q = 0; q < P; ++q) {
+    best[q] = 0u;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) best[q] = max(best[q], key[q][i]);
+    m[q] = __reduce_max_sync(0xffffffffu, best[q]);
+    id[q] = -1;
+    mine[q] = 0u;
+    all[q] = 0.f;
+  }
+#pragma unroll
+  for (int q = 0; q < P; ++q) top[q] = m[q];
+  if (!a.renorm) {  // the sum over all experts, while every key is still there
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const float mx = key_value(top[q]);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (key[q][i]) all[q] += key[q][i] == top[q] ? 1.f : expf(key_value(key[q][i]) - mx);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int q = 0; q < P; ++q) all[q] += __shfl_xor_sync(0xffffffffu, all[q], o);
+  }
   for (int j = 0; j < a.k; ++j) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-    if (m == 0u) break;  // nothing unmasked is left
-    if (j == 0) {
-      top = m;
-      if (!a.renorm) {  // the sum over all experts, while every key is still there
-        const float mx = key_value(top);
+    int e[P], win[P];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (key[i]) all += key[i] == top ? 1.f : expf(key_value(key[i]) - mx);
+    for (int q = 0; q < P; ++q) {
+      e[q] = kRouteMaxE;
+      if (best[q] == m[q]) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        for (int i = EPL - 1; i >= 0; --i)
+          if (key[q][i] == m[q]) e[q] = lane + 32 * i;
       }
     }
-    int e = kRouteMaxE;
-    if (best == m) {
 #pragma unroll
-      for (int i = EPL - 1; i >= 0; --i)
-        if (key[i] == m) e = lane + 32 * i;
-    }
-    const int win = __reduce_min_sync(0xffffffffu, e);
-    if (lane == j) {
-      id = win;
-      mine = m;
-    }
-    if (win == e && best == m) {  // this lane's expert was taken
-      best = 0u;
+    for (int q = 0; q < P; ++q) win[q] = __reduce_min_sync(0xffffffffu, e[q]);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        if (lane + 32 * i == win) key[i] = 0u;
-        best = max(best, key[i]);
+    for (int q = 0; q < P; ++q) {
+      if (lane == j && m[q] != 0u) {  // 0: nothing unmasked is left
+        id[q] = win[q];
+        mine[q] = m[q];
+      }
+      if (win[q] == e[q]) {  // this lane's expert was taken (or every key is 0 already)
+        best[q] = 0u;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (lane + 32 * i == win[q]) key[q][i] = 0u;
+          best[q] = max(best[q], key[q][i]);
+        }
       }
     }
+#pragma unroll
+    for (int q = 0; q < P; ++q) m[q] = __reduce_max_sync(0xffffffffu, best[q]);
   }
-  float p = 0.f;
-  if (id >= 0) p = mine == top ? 1.f : expf(key_value(mine) - key_value(top));
+  float p[P];
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    p[q] = 0.f;
+    if (id[q] >= 0) p[q] = mine[q] == top[q] ? 1.f : expf(key_value(mine[q]) - key_value(top[q]));
+    if (a.renorm) all[q] = p[q];
+  }
   if (a.renorm) {
-    all = p;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int q = 0; q < P; ++q) all[q] += __shfl_xor_sync(0xffffffffu, all[q], o);
   }
-  w = id >= 0 ? p / all : 0.f;
+#pragma unroll
+  for (int q = 0; q < P; ++q) w[q] = id[q] >= 0 ? p[q] / all[q] : 0.f;
 }
 
 // Shared memory of a block: running counts of its experts before the current tile, and
@@ -141,38 +168,41 @@ struct RouteSmem {
 // Choices and ranks of tokens [t0, t1): writes ids and weights, and into slots the rank of
 // every pair among the block's pairs of its expert (-1 for a masked place).  On return
 // sm.base[e] counts the block's pairs.
-template <typename L, int EPL>
+template <typename L, int EPL, int P>
 __device__ __forceinline__ void choose_and_rank(const RouteArgs& a, int t0, int t1, RouteSmem& sm) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kPer = kRouteTile / kRouteWarps;  // tokens of a warp in a tile
+  constexpr int kTile = P * kRouteWarps;  // tokens ranked together: P of a warp
   for (int e = tid; e < a.E; e += kRouteThreads) sm.base[e] = 0;
-  for (int tile = t0; tile < t1; tile += kRouteTile) {
-    for (int i = tid; i < kRouteWarps * a.E; i += kRouteThreads) sm.cnt[i / a.E][i % a.E] = 0;
-    __syncthreads();
-    int id[kPer], rank[kPer];
-    uint32_t key[kPer][EPL];  // the logits of the warp's tokens are loaded together
+  for (int tile = t0; tile < t1; tile += kTile) {
+    uint32_t key[P][EPL];  // the logits of the warp's tokens are loaded together
 #pragma unroll
-    for (int q = 0; q < kPer; ++q)
-      if (tile + kPer * warp + q < t1) load_keys<L, EPL>(a, tile + kPer * warp + q, lane, key[q]);
+    for (int q = 0; q < P; ++q) {
+      if (tile + P * warp + q < t1) {
+        load_keys<L, EPL>(a, tile + P * warp + q, lane, key[q]);
+      } else {
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int t = tile + kPer * warp + q;
-      id[q] = -1;
-      rank[q] = 0;
-      if (t < t1) {
-        float w;
-        choose<EPL>(a, key[q], lane, id[q], w);
-        if (lane < a.k) {
-          a.ids[(int64_t)t * a.k + lane] = id[q];
-          a.weights[(int64_t)t * a.k + lane] = w;
-        }
-        // a token's experts are distinct, so its pairs do not rank against each other
-        if (id[q] >= 0) {
-          rank[q] = sm.cnt[warp][id[q]];
-          sm.cnt[warp][id[q]] = rank[q] + 1;
-        }
-        __syncwarp();
+        for (int i = 0; i < EPL; ++i) key[q][i] = 0u;
       }
+    }
+    for (int e = lane; e < a.E; e += 32) sm.cnt[warp][e] = 0;
+    __syncwarp();
+    int id[P], rank[P];
+    float w[P];
+    choose<EPL, P>(a, key, lane, id, w);
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const int t = tile + P * warp + q;
+      rank[q] = 0;
+      if (t < t1 && lane < a.k) {
+        a.ids[(int64_t)t * a.k + lane] = id[q];
+        a.weights[(int64_t)t * a.k + lane] = w[q];
+      }
+      // a token's experts are distinct, so its pairs do not rank against each other
+      if (id[q] >= 0) {
+        rank[q] = sm.cnt[warp][id[q]];
+        sm.cnt[warp][id[q]] = rank[q] + 1;
+      }
+      __syncwarp();
     }
     __syncthreads();
     for (int e = tid; e < a.E; e += kRouteThreads) {  // exclusive scan over the warps, on top of base
@@ -187,8 +217,8 @@ __device__ __forceinline__ void choose_and_rank(const RouteArgs& a, int t0, int 
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int t = tile + kPer * warp + q;
+    for (int q = 0; q < P; ++q) {
+      const int t = tile + P * warp + q;
       if (t < t1 && lane < a.k)
         a.slots[(int64_t)t * a.k + lane] = id[q] >= 0 ? sm.cnt[warp][id[q]] + rank[q] : -1;
     }
@@ -232,12 +262,13 @@ __device__ __forceinline__ void place_pairs(const RouteArgs& a, int t0, int t1, 
   }
 }
 
-template <typename L, int EPL, bool kOne>
+// P: tokens of a warp at a time.  kOne: this block does everything.
+template <typename L, int EPL, int P, bool kOne>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
   __shared__ RouteSmem sm;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int t0 = blockIdx.x * a.tokens_per_block, t1 = min(a.T, t0 + a.tokens_per_block);
-  choose_and_rank<L, EPL>(a, t0, t1, sm);
+  choose_and_rank<L, EPL, P>(a, t0, t1, sm);
   if (kOne) {
     __syncthreads();
     const int sum = scan_experts(sm.base, a.E, sm.scan);
@@ -263,6 +294,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(RouteArgs a)
   const int e = tid % a.E, pt = tid / a.E;
   if (pt < parts) {
     int b = 0, s = 0;
+#pragma unroll 8
     for (int i = pt; i < nb; i += parts) {
       const int c = a.counts[(int64_t)i * a.E + e];
       if (i < (int)blockIdx.x) b += c;
@@ -309,12 +341,14 @@ static cudaError_t launch_route_t(RouteArgs a, cudaStream_t s) {
   const int blocks = route_blocks(a.T);
   if (blocks == 1) {
     a.tokens_per_block = a.T;
-    return launch_pdl(route_kernel<L, EPL, true>, 1, a, s);
+    // up to a token a warp, the other three would only be instructions
+    return a.T <= kRouteWarps ? launch_pdl(route_kernel<L, EPL, 1, true>, 1, a, s)
+                              : launch_pdl(route_kernel<L, EPL, kRoutePer, true>, 1, a, s);
   }
   const int tiles = (a.T + kRouteTile - 1) / kRouteTile;
   a.tokens_per_block = (tiles + blocks - 1) / blocks * kRouteTile;
   const int grid = (a.T + a.tokens_per_block - 1) / a.tokens_per_block;
-  cudaError_t e = launch_pdl(route_kernel<L, EPL, false>, grid, a, s);
+  cudaError_t e = launch_pdl(route_kernel<L, EPL, kRoutePer, false>, grid, a, s);
   return e != cudaSuccess ? e : launch_pdl(route_place_kernel, grid, a, s);
 }
 
