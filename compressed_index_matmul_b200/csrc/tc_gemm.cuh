@@ -605,6 +605,18 @@ struct TcGeom {
   bool dual;  // two CTAs per SM (2 decode warps per lane quarter; 3 stages for 64-token tiles)
 };
 
+// Estimated time in us of a forward cut into S splits of K, the fixed part left out: the 128-input
+// slices that a CTA decodes one after the other (0.8 us each, 1.2 with 16-bit indices; two CTAs that
+// share an SM take 1.7 times as long), and the sum over the splits: a cluster pair exchanges half
+// of its sums over distributed shared memory, more splits write theirs to global memory, from where
+// the last CTA of a tile reads them all, a split after the other.  Fitted to 20 layer shapes from
+// 1003 x 960 to 4096 x 14336 at M = 8 to 300, each forced to 1, 2, 3, 4 and 8 splits.
+static float tc_split_cost(const TcGeom& g, int S, bool k16, bool pair_ok, int nsl, int num_sms) {
+  const int sps = (nsl + S - 1) / S, n = (nsl + sps - 1) / sps;
+  const float decode = (k16 ? 1.2f : 0.8f) * (float)sps * (g.RT * g.TT * n > num_sms ? 1.7f : 1.f), T = (float)g.T;
+  return decode + (n == 1 ? 0.f : n == 2 && pair_ok ? 0.4f + 0.01f * T : T * (0.033f + 0.0163f * (float)n));
+}
+
 // fmt: kFmt* (the same values as VQ_FMT_*).
 static TcGeom tc_geom(int fmt, int M, int N, int K, int num_sms) {
   TcGeom g;
@@ -629,6 +641,13 @@ static TcGeom tc_geom(int fmt, int M, int N, int K, int num_sms) {
     g.dual = false;
     S = splits(num_sms);
   }
+  // The split that costs least, among those that fit the SMs.  With as many as fit, us: 2048 x 2048
+  // M = 256 48.5, with the 2 chosen 14.4; M = 100 25.8, with 2 12.6; 1003 x 960 M = 77 18.8, with 1 9.7;
+  // 4096 x 4096 M = 128 24.1, with 2 19.5; M = 16 16.1, with 4 14.6.  4096 x 14336 M = 16 keeps its 8
+  // (29.1; 30.9 with 4), 4096 x 4096 M = 8 on 16-bit indices its 4 (17.8; 25.0 with 2).
+  const bool k16 = fmt == kFmtVq16 || fmt == kFmtVq16Rvq;
+  for (int s = S - 1; s >= 1; --s)
+    if (tc_split_cost(g, s, k16, N % 8 == 0, nsl, num_sms) < tc_split_cost(g, S, k16, N % 8 == 0, nsl, num_sms)) S = s;
   const int sps = (nsl + S - 1) / S;
   g.S = (nsl + sps - 1) / sps;
   g.kps = sps * 128;
