@@ -552,8 +552,14 @@ __global__ void __launch_bounds__(kXtThreads, 1)
           }
         }
         if (kStaged) {
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(idx_empty(part));
+          // The slot is free once every lane's bytes are in its registers.  Which lane says so depends
+          // on the bytes, so that no load can be moved behind the arrival: with lane 0 arriving after a
+          // __syncwarp, the scales of 16-bit layers were at times those of four slices later.
+          uint32_t seen = sc2;
+#pragma unroll
+          for (int i = 0; i < (k16 ? 8 : 4); ++i) seen ^= lo[i];
+          if (!k16) seen ^= hi[0] ^ hi[1] ^ s2[0] ^ s2[1];
+          if (lane == (int)(__reduce_or_sync(0xffffffffu, seen) & 31u)) ptx::mbar_arrive(idx_empty(part));
         }
         bool waited = round == 0;  // the MMAs of this stage's slice before are done
 #pragma unroll

@@ -117,6 +117,11 @@ SHAPES = [
     (2, 512, 2048, FMT_RVQ12_4, 64, DT_BF16, [300, 40]),
     (6, 72, 256, FMT_VQ16, 64, DT_BF16, [2, 0, 31, 8, 0, 64]),
     (3, 136, 448, FMT_VQ16, 0, DT_F16, [18, 257, 1]),
+    # more slices of K than index slots, block scales: a slot is refilled while its neighbours decode
+    (4, 512, 1280, FMT_VQ16, 64, DT_F16, [128, 128, 128, 128]),
+    (3, 528, 1472, FMT_VQ16, 64, DT_BF16, [200, 60, 100]),
+    (4, 512, 1472, FMT_RVQ12, 64, DT_F16, [128, 64, 128, 20]),
+    (4, 512, 1280, FMT_RVQ12_4, 64, DT_F16, [128, 128, 128, 128]),
     (40, 48, 128, FMT_RVQ12_4, 64, DT_BF16, [i % 4 for i in range(40)]),  # a block meets many experts
 ]
 
