@@ -21,8 +21,9 @@ namespace vq {
 
 // The code is kept small, and what a call has no tensor for is jumped over: every forward kernel
 // holds it at each of its stores, unrolled over the values of a thread, and a short forward
-// waits for instructions that the SM has not run yet (1003 x 960 at M = 77 with bias and GELU: 24.4
-// us with every activation and load unrolled and predicated, 22.2 so, 18.0 without an epilogue;
+// waits for instructions that the SM has not run yet (1003 x 960 at M = 77 in 8 splits of K with bias
+// and GELU: 24.4 us with every activation and load unrolled and predicated, 22.2 so, 18.0 without an
+// epilogue; in the one split now taken 14.2 and 9.5;
 // 8192 x 8192 at M = 1024 with bias, GELU and residual: 151 against 134 us, 120 without).  Hence one
 // formula for two activations, and a call for the erf form.
 struct ActParams {

@@ -142,7 +142,7 @@ __device__ __forceinline__ void decode_scaled(const uint4& c1, const uint32_t (&
   }
 }
 
-// Row `c` of the tile and its bias: act(f + b), or act(gate + bg) * (up + bu).
+// One output of a gated matrix; gate and up have their bias.
 __device__ __forceinline__ float gated(int act, float gate, float up) { return apply_act(act, gate) * up; }
 
 }  // namespace vq
