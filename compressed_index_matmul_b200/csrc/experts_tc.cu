@@ -49,7 +49,7 @@ constexpr int kXtStages = 4;                           // x stages of a slice (1
 constexpr int kXtMaxT = 256;
 constexpr int kXtSlots = kXtParts;                     // index slices in flight
 constexpr uint32_t kXtACols = 64;                      // TMEM columns of one A stage (128 k of 16-bit pairs)
-constexpr uint32_t kXtIdxHi = 2048, kXtIdxS2 = 3072, kXtIdxSc = 4096, kXtIdxSlot = 4608;
+constexpr uint32_t kXtIdxHi = 16 * kXtRows, kXtIdxS2 = 24 * kXtRows, kXtIdxSc = 32 * kXtRows, kXtIdxSlot = 36 * kXtRows;  // bytes
 constexpr uint32_t kXtOffTiles = 65536;                // after the codebook
 constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 16;
 constexpr uint32_t kXtOffIdx = kXtOffBars + 768;

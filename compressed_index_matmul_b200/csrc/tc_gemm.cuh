@@ -66,7 +66,7 @@ __host__ __device__ constexpr int tc_threads(int parts) { return 64 + 32 * 4 * p
 constexpr int kTcMaxT = 256;
 constexpr uint32_t kTcACols = 32;   // TMEM columns of one A stage (64 k of 16-bit pairs)
 // index-slice ring slot: lo 16 B, hi4 8 B, s2 8 B, scales 4 B per row (idx16: 32 B per row)
-constexpr uint32_t kTcIdxLo = 0, kTcIdxHi = 2048, kTcIdxS2 = 3072, kTcIdxSc = 4096;
+constexpr uint32_t kTcIdxLo = 0, kTcIdxHi = 2048, kTcIdxS2 = kTcIdxHi + 1024, kTcIdxSc = 4096;
 constexpr uint32_t kTcIdxSlot = 4608;
 constexpr int kTcIdxSlots = 4;
 constexpr uint32_t kTcOffBars = 65536;   // after the 64 KiB codebook
