@@ -11,11 +11,11 @@
 // expert, and with it the codebook in shared memory, once or twice.
 //   warp 0     lane 0: x, per 128-input slice, a TMA load per 64 inputs of the block's half of the
 //              tile's x rows (a box of 32, 64 or 128 rows, 128-byte swizzle: one large load
-//              instead of several small ones) into a ring of four stages
+//              instead of several small ones) into a ring of four stages.  Both blocks' loads
+//              complete on the first block's barrier, where the MMAs are issued
 //   warp 1     allocates TMEM; in the first block an elected lane issues tcgen05.mma (M = 256, N =
 //              the tile's rows rounded up to 16, K = 16), A from both blocks' TMEM, B from both
-//              blocks' shared memory, and commits each stage to both; the second block's passes
-//              its x stages' arrivals on
+//              blocks' shared memory, and commits each stage to both
 //   warp 2     the expert's 12-bit codebook (one bulk copy when it changes) and, per
 //              128-input slice, the index bytes of the block's rows (one contiguous run per
 //              plane; glu: two; a lane each) into a ring of four slots
@@ -87,11 +87,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Arrive on a barrier of block `rank` of the pair.  What the arrivals tell of is in TMEM and in the
-// async proxy's shared memory, ordered by the tcgen05 fences, so the cheap default scope serves (a
-// release at cluster scope held each decode warp up for more than 1000 cycles).
+// Arrive on a barrier of block `rank` of the pair.  What the arrivals tell of is in TMEM (decoded
+// weights stored, sums read), ordered by the tcgen05 fences on both sides, so the cheap default scope
+// serves (a release at cluster scope held each decode warp up for more than 1000 cycles).
 __device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ptx::map_shared_rank(bar, rank)) : "memory");
+}
+// A 2-D tensor load into this block's shared memory that completes on `bar`, a barrier of either block
+// of the pair (an address from map_shared_rank): the thread that waits there sees the bytes
+// of both blocks landed, with nothing in between to pass their arrival on.
+__device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
 }
 // The pair's TMEM and MMA (cta_group::2; both blocks allocate and free).
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
@@ -145,8 +155,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   auto empty_a = [&](int s) { return bar1 + 8u * (kXtParts + s); };
   auto idx_full = [&](int s) { return bar1 + 8u * (2 * kXtParts + s); };
   auto idx_empty = [&](int s) { return bar1 + 8u * (3 * kXtParts + s); };
-  auto peer_b = [&](int s) { return bar1 + 8u * (4 * kXtParts + s); };  // the second block's x stage (first block only)
-  static_assert(8 * (3 * kSt + 6 + 4 * kXtParts) <= 384, "barriers overlap the flags");
+  static_assert(8 * (2 * kSt + 6 + 4 * kXtParts) <= 384, "barriers overlap the flags");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kXtOffBars + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kXtOffBars + 388);
   int* part_sums = reinterpret_cast<int*>(sm + kXtOffBars + 392);  // 2 per warp
@@ -165,10 +174,8 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   const uint32_t tcols = 512u;  // acol0 + kXtParts * kXtACols is above 256
 
   if (tid == 0) {
-    for (int s = 0; s < kSt; ++s) {
-      ptx::mbar_init(full_b(s), 1);  // the x warp's expect_tx arrival (+ bytes)
-      ptx::mbar_init(peer_b(s), 1);  // passed on by the second block
-    }
+    for (int s = 0; s < kSt; ++s)
+      ptx::mbar_init(full_b(s), 1);  // the first block's expect_tx arrival (+ both blocks' bytes; first block only)
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(acc_full(b), 1);
       ptx::mbar_init(acc_empty(b), 2 * kXtDecode);  // both blocks' decode warps (first block only)
@@ -272,13 +279,19 @@ __global__ void __launch_bounds__(kXtThreads, 1)
             ok = false;
             break;
           }
+          // The second block's bytes may land before the first block expects them: the phase cannot
+          // end without its arrival, and the next one's loads wait for the MMAs of this one.
           const int blocks = slice_width(j, G) / 8;
-          ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)(blocks * box) * 128u);
-          for (int h = 0; h < blocks; ++h) ptx::tma_load_2d(b_tile(s, h), map, 128 * j + 64 * h, first, full_b(s));
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full_b(s), (uint32_t)(2 * blocks * box) * 128u);
+          const uint32_t bar = ptx::map_shared_rank(full_b(s), 0);
+          for (int h = 0; h < blocks; ++h) pair_tma_load_2d(b_tile(s, h), map, 128 * j + 64 * h, first, bar);
         }
       }
-      // Do not leave while a copy into this block's shared memory may be in flight.
-      for (int i = js > kSt ? js - kSt : 0; i < js; ++i) ptx::mbar_wait(full_b(i % kSt), (i / kSt) & 1, a.err);
+      // Do not leave while a copy into this block's shared memory may be in flight: the MMAs of the
+      // last slices come after both blocks' copies (and if they never come, the copies have had the
+      // waits' second).
+      for (int i = js > kSt ? js - kSt : 0; i < js; ++i)
+        ptx::mbar_wait(empty_a(i % kXtParts), (i / kXtParts) & 1, a.err);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the first block's)
@@ -289,16 +302,6 @@ __global__ void __launch_bounds__(kXtThreads, 1)
     const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
     int js = 0, ui = 0;
-    if (rank == 1) {  // tell the first block which of this block's x stages have landed
-      const int n = (uend - ubeg) * nsl;
-      for (; js < n; ++js) {
-        if (!ptx::mbar_wait(full_b(js % kSt), (js / kSt) & 1, a.err)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) arrive_at(peer_b(js % kSt), 0);
-      }
-    }
     for (int u = ubeg; rank == 0 && ok && u < uend; ++u, ++ui) {
       const XtTile t = tile_of(u);
       const uint32_t idesc = __shfl_sync(0xffffffffu, ptx::idesc_f16(kAbFmt, 2 * kXtRows, (uint32_t)t.T), 0);
@@ -315,12 +318,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
           par = (uint32_t)(js / kSt) & 1u;
           wait = true;
         }
-        if (lane == 2) {
-          bar = peer_b(s);
-          par = (uint32_t)(js / kSt) & 1u;
-          wait = true;
-        }
-        if (lane == 3 && j == 0 && ui >= nacc) {  // the decode warps have read the accumulator's last tile
+        if (lane == 2 && j == 0 && ui >= nacc) {  // the decode warps have read the accumulator's last tile
           bar = acc_empty(b);
           par = (uint32_t)((ui / nacc) - 1) & 1u;
           wait = true;
@@ -348,10 +346,10 @@ __global__ void __launch_bounds__(kXtThreads, 1)
       }
     }
     if (!ok) *abort_flag = 1;
-    // The last commit covers every MMA before it and lands in both blocks: wait for it, so that
-    // TMEM and shared memory are not released under one (on a whole run the decode warps have
-    // waited already).
-    if (js && (rank == 0 || ok)) ptx::mbar_wait(empty_a((js - 1) % kXtParts), ((js - 1) / kXtParts) & 1, a.err);
+    // The last commit covers every MMA before it: wait for it, so that neither block, which this warp
+    // joins at the barrier below, releases TMEM or shared memory under one (on a whole run the decode
+    // warps have waited already).
+    if (js) ptx::mbar_wait(empty_a((js - 1) % kXtParts), ((js - 1) / kXtParts) & 1, a.err);
   } else if (warp == 2) {
     // ------------------------------------------------------------ codebooks and index slices
     // Lane 4 h + p copies plane p (lo or idx16, hi4, s2, scales) of run h of the tile's rows (glu: the
