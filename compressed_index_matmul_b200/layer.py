@@ -30,9 +30,12 @@ def _new(shape, dtype, device, stream=None):
     that stream's memory: a block freed on another one may still be in use there."""
     import torch
 
-    if stream is None:
+    raw = None if stream is None else _raw_stream(stream, device.index)
+    if raw is None or raw == _raw_stream(None, device.index):
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(_raw_stream(stream, device.index), device=device)):
+    # ExternalStream takes 0, the default stream's handle, for none given and gives a pool stream's memory
+    of = torch.cuda.default_stream(device) if raw == 0 else torch.cuda.ExternalStream(raw, device=device)
+    with torch.cuda.stream(of):
         return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -1,0 +1,47 @@
+"""GPU test: a result for the default stream, given explicitly, lies in the default stream's memory."""
+
+import pytest
+import torch
+
+import compressed_index_matmul_b200 as vq
+from synth import DT_BF16, FMT_RVQ12_4
+from tests.gpu_util import require_gpu
+from tests.test_gpu_experts import make_experts, offsets_of, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def test_the_default_stream_given_from_another_stream():
+    """A block just freed on the default stream is the next result's, whichever stream is current; a
+    block freed on the current one is not."""
+    E, N, K, T = 2, 64, 128, 16
+    _, arrays = make_experts(E, N, K, FMT_RVQ12_4, 64, 22)
+    X = vq.VQExperts(E, N, K, FMT_RVQ12_4, 64, DT_BF16, T, arrays)
+    L = vq.VQLinear(N, K, FMT_RVQ12_4, 64, DT_BF16, T, {k: v[0] for k, v in arrays.items()})
+    R = vq.VQRouter(E, 1, T)
+    x, off, logits = randn((T, K), DT_BF16, 1), offsets_of([8, 8]), torch.zeros((T, E), device="cuda")
+    r, side = R.forward(logits), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda s: X.forward(x, off, stream=s), lambda s: L.forward_fused(x, stream=s),
+                 lambda s: R.forward(logits, stream=s).weights, lambda s: vq.combine(x, r.weights, r.slots, stream=s)):
+        first = call(None)
+        at = first.data_ptr()
+        del first
+        with torch.cuda.stream(side):
+            here = call(None)
+            assert here.data_ptr() != at
+            side_at = here.data_ptr()
+            del here
+            for s in (torch.cuda.default_stream(), 0):
+                got = call(s)
+                assert got.data_ptr() == at and got.data_ptr() != side_at
+                del got
+            again = call(side)
+            assert again.data_ptr() == side_at
+            del again
+        torch.cuda.synchronize()
