@@ -101,11 +101,9 @@ class VQLinear:
         return torch.bfloat16 if self.act_dtype == B.VQ_BF16 else torch.float16
 
     def forward(self, x, y=None, stream=None):
-        import torch
-
         M = x.shape[0]
         if y is None:
-            y = torch.empty((M, self.N), dtype=self.torch_dtype, device=self.device)
+            y = _new((M, self.N), self.torch_dtype, self.device, stream)
         B.vq_linear_forward(self.handle, x, self.planes, self.codebooks, self.t["scales"], y, M, self.N, self.K,
                             stream)
         return y
@@ -114,11 +112,9 @@ class VQLinear:
 
     def forward_rotated(self, x, signs, y=None, stream=None):
         """y = rotate(x) . W^T (vq_linear_forward_rotated); `signs` is an int8 tensor of +-1 [K]."""
-        import torch
-
         M = x.shape[0]
         if y is None:
-            y = torch.empty((M, self.N), dtype=self.torch_dtype, device=self.device)
+            y = _new((M, self.N), self.torch_dtype, self.device, stream)
         B.vq_linear_forward_rotated(self.handle, x, signs, self.planes, self.codebooks, self.t["scales"], y, M, self.N,
                                     self.K, stream)
         return y

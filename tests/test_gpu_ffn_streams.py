@@ -45,3 +45,21 @@ def test_the_default_stream_given_from_another_stream():
             assert again.data_ptr() == side_at
             del again
         torch.cuda.synchronize()
+
+
+def test_plain_forwards_for_another_stream():
+    N, K, T = 64, 128, 16
+    _, arrays = make_experts(1, N, K, FMT_RVQ12_4, 64, 23)
+    L = vq.VQLinear(N, K, FMT_RVQ12_4, 64, DT_BF16, T, {k: v[0] for k, v in arrays.items()}, rht=1)
+    x, signs, side = randn((T, K), DT_BF16, 1), torch.ones(K, dtype=torch.int8, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda s: L.forward(x, stream=s), lambda s: L.forward_rotated(x, signs, stream=s)):
+        here = call(None)
+        at = here.data_ptr()
+        del here
+        for s in (side, side.cuda_stream):
+            assert call(s).data_ptr() != at
+        with torch.cuda.stream(side):
+            for s in (torch.cuda.default_stream(), 0):
+                assert call(s).data_ptr() == at
+        torch.cuda.synchronize()
