@@ -24,7 +24,7 @@ bool plan_vq16(const vq_linear_desc& d, const DeviceInfo& dev, int M, Plan* p);
 }  // namespace vq
 
 struct vq_linear_s {
-  vq_linear_desc d;
+  vq_linear_desc d;  // first: the host tests of the argument checks make up a handle from it
   vq::DeviceInfo dev;
   int path;
   float* scratch;
@@ -175,6 +175,35 @@ cudaError_t free_on_device(int device, void* a, void* b) {
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
+}
+
+vq_status check_output(const vq_linear_desc& d, const vq_planes& p, const vq_codebooks& cb, const void* scales, int E,
+                       int sets, const void* y, size_t yb) {
+  const bool ladder = d.fmt == VQ_FMT_VQ16_RVQ, k16 = d.fmt == VQ_FMT_VQ16 || ladder, two = d.fmt == VQ_FMT_RVQ12_4;
+  const size_t n = (size_t)E * d.N * (d.K / 8), big = (size_t)sets * (k16 ? 65536 : 4096) * 16;
+  // what the format does not read has no bytes
+  const struct {
+    const void* p;
+    size_t bytes;
+    const char* name;
+  } in[] = {{p.lo, k16 ? 0 : n, "planes->lo"},
+            {p.hi4, k16 ? 0 : n / 2, "planes->hi4"},
+            {p.s2, two ? n / 2 : 0, "planes->s2"},
+            {p.idx16, k16 ? 2 * n * (ladder ? d.n16 : 1) : 0, "planes->idx16"},
+            {p.idx8, ladder && d.n8 ? n : 0, "planes->idx8"},
+            {p.corr_rows, d.corr ? sizeof(int32_t) * ((size_t)d.N + 1) : 0, "planes->corr_rows"},
+            {p.corr_cols, d.corr && p.corr_cols ? sizeof(int32_t) : 0, "planes->corr_cols"},
+            {p.corr_vals, d.corr && p.corr_vals ? sizeof(uint16_t) : 0, "planes->corr_vals"},
+            {cb.cb1, big, "codebooks->cb1"},
+            {cb.cb2, two ? (size_t)sets * 256 : 0, "codebooks->cb2"},
+            {cb.cbr[0], ladder && d.n16 > 1 ? big : 0, "codebooks->cbr[0]"},
+            {cb.cbr[1], ladder && d.n16 > 2 ? big : 0, "codebooks->cbr[1]"},
+            {cb.cbr[2], ladder && d.n16 > 3 ? big : 0, "codebooks->cbr[2]"},
+            {cb.cb8, ladder && d.n8 ? (size_t)sets * 4096 : 0, "codebooks->cb8"},
+            {scales, (size_t)E * d.N * (d.scale_group == 64 ? d.K / 64 : 1) * 2, "scales"}};
+  for (const auto& q : in)
+    if (q.bytes && overlaps(q.p, q.bytes, y, yb)) return fail(VQ_ERR_INVALID_ARG, "y overlaps %s", q.name);
+  return VQ_OK;
 }
 
 vq::LayerArgs make_args(const vq_linear_desc& d, const vq_planes* p, const vq_codebooks* cb, const void* scales) {
@@ -568,6 +597,8 @@ VQ_API vq_status vq_linear_forward_epilogue(vq_linear_t h, const void* x, const 
     if (parts[i].p && parts[i].p != y && overlaps(parts[i].p, ybytes, y, ybytes))
       return fail(VQ_ERR_INVALID_ARG, "y partially overlaps %s", parts[i].name);
   if (M == 0) return VQ_OK;
+  if (rotated && overlaps(signs, (size_t)K, y, ybytes)) return fail(VQ_ERR_INVALID_ARG, "y overlaps signs");
+  if ((st = check_output(h->d, *planes, *codebooks, scales, 1, 1, y, ybytes))) return st;
   if ((st = check_device(h))) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return rotated ? run_forward_rotated(h, x, signs, planes, codebooks, scales, epi, y, M, K, s)

@@ -28,5 +28,10 @@ vq_status refuse_alloc();
 cudaError_t free_on_device(int device, void* a, void* b = nullptr);
 // Whether the byte ranges [a, a + na) and [b, b + nb) meet.
 bool overlaps(const void* a, size_t na, const void* b, size_t nb);
+// VQ_ERR_INVALID_ARG where y's yb bytes meet a plane, codebook or scale that a call with these (valid)
+// arguments reads: those of E layers after one another, with `sets` sets of codebooks.  Of the sparse
+// correction's entries only the first counts, for their number is on the device.
+vq_status check_output(const vq_linear_desc& d, const vq_planes& p, const vq_codebooks& cb, const void* scales, int E,
+                       int sets, const void* y, size_t yb);
 
 }  // namespace vq

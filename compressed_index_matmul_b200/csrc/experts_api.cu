@@ -13,7 +13,7 @@ cudaError_t launch_experts_tc(const ExpertsArgs& a, void* xs, int Tmax, int num_
 using namespace vq;
 
 struct vq_experts_s {
-  vq_experts_desc d;
+  vq_experts_desc d;  // first, as in vq_linear_s
   DeviceInfo dev;
   int path;
   uint32_t* err;  // device word, set by bounded waits that gave up
@@ -149,6 +149,7 @@ VQ_API vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_row
   if (overlaps(offsets, sizeof(int32_t) * (h->d.E + 1), y, yb) || (rows && overlaps(rows, sizeof(int32_t) * T, y, yb)) ||
       (bias && overlaps(bias, (size_t)h->d.E * d.N * 2, y, yb)))
     return fail(VQ_ERR_INVALID_ARG, "y overlaps offsets, rows or bias");
+  if ((st = check_output(d, *planes, *codebooks, scales, h->d.E, h->d.shared_codebooks ? 1 : h->d.E, y, yb))) return st;
   if ((st = check_current_device(h->dev.device))) return st;
   ExpertsArgs a{};
   a.w = make_args(d, planes, codebooks, scales);

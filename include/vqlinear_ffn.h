@@ -49,7 +49,8 @@ typedef struct {
  * errors as those two; bias, mul and residual are read once, and an epilogue with act
  * VQ_ACT_NONE and no tensors gives their result bit for bit.
  * mul and residual may be y itself (each element is read before it is written); any other
- * overlap of y with an input is VQ_ERR_INVALID_ARG, as is an `act` that is not a VQ_ACT_*
+ * overlap of y with an input is VQ_ERR_INVALID_ARG (of the sparse correction's entries the first
+ * is looked at: the host does not know their number), as is an `act` that is not a VQ_ACT_*
  * or a NULL `epi`. */
 vq_status vq_linear_forward_epilogue(vq_linear_t h, const void* x, const int8_t* signs, const vq_planes* planes,
                                      const vq_codebooks* codebooks, const void* scales, const vq_epilogue* epi,
@@ -96,7 +97,7 @@ vq_status vq_experts_destroy(vq_experts_t h);
  *            bad offsets give wrong rows but no access out of range.
  *   bias     [E][N], act_dtype, or NULL
  *   y        [T][N] (glu: [T][N/2]), act_dtype.  Rows below offsets[0] or from offsets[E]
- *            on are left as they were.  y must not overlap any input.
+ *            on are left as they were.  A y that overlaps an input is VQ_ERR_INVALID_ARG.
  * Accumulation is fp32.  The weights are rounded to act_dtype before the product, as
  * the single-layer paths that materialise weights do (the scaled stage sum with one fused
  * multiply-add per stage in fp32).  For a given kernel (below) the result of a row does not
