@@ -35,8 +35,9 @@ class VQExperts:
 
     ``arrays``: numpy arrays or torch tensors named as in ``VQLinear`` (lo, hi4, s2, idx16, idx8,
     cb1, cb2, cbr, cb8, scales, mult), each with a leading dimension E in include/vqlinear.h's
-    storage format; the codebooks' is 1 (or left out) with `shared_codebooks`.  For the residual
-    ladder cbr is [n16 - 1, E or 1, 65536, 8] and idx16 [E, n16 * N * K / 8].
+    storage format; the codebooks' is 1 (or left out) with `shared_codebooks`.  Index planes are
+    8-bit or 16-bit integers, codebooks and scales float16 or its bits in 16-bit integers.  For the
+    residual ladder cbr is [n16 - 1, E or 1, 65536, 8] and idx16 [E, n16 * N * K / 8].
     `glu`: rows [0, N/2) of every matrix are a gate, the others its up projection, and the output
     has N/2 columns, act(gate) * up.  `act` is a VQ_ACT_*, `bias` [E, N] or None.
     A call takes at most `max_rows` rows, all experts together.  `gather`: calls may pass `rows`,
@@ -59,21 +60,24 @@ class VQExperts:
         self.n16 = t["idx16"].numel() // (E * n) if ladder and "idx16" in t else 0
         self.n8 = int(ladder and "idx8" in t)
         self.mult = tuple(float(m) for m in np.asarray(arrays["mult"], dtype=np.float32)) if ladder else ()
-        want = {"scales": (E * N * (1 if scale_group == K else K // 64), 2), "cb1": (sets * (65536 if k16 else 4096) * 8, 2)}
+        byte, index16 = (torch.uint8, torch.int8), (torch.int16, torch.uint16)
+        half = (torch.float16, *index16)  # or its bits
+        want = {"scales": (E * N * (1 if scale_group == K else K // 64), half),
+                "cb1": (sets * (65536 if k16 else 4096) * 8, half)}
         if k16:
-            want["idx16"] = (E * n * max(1, self.n16), 2)
+            want["idx16"] = (E * n * max(1, self.n16), index16)
         else:
-            want |= {"lo": (E * n, 1), "hi4": (E * n // 2, 1)}
+            want |= {"lo": (E * n, byte), "hi4": (E * n // 2, byte)}
         if fmt == B.VQ_FMT_RVQ12_4:
-            want |= {"s2": (E * n // 2, 1), "cb2": (sets * 16 * 8, 2)}
+            want |= {"s2": (E * n // 2, byte), "cb2": (sets * 16 * 8, half)}
         if ladder and self.n16 > 1:
-            want["cbr"] = ((self.n16 - 1) * sets * 65536 * 8, 2)
+            want["cbr"] = ((self.n16 - 1) * sets * 65536 * 8, half)
         if self.n8:
-            want |= {"idx8": (E * n, 1), "cb8": (sets * 256 * 8, 2)}
-        for name, (count, size) in want.items():
-            if name not in t or t[name].numel() != count or t[name].element_size() != size:
-                raise ValueError(f"{name} must have {count} entries of {size} bytes for E={E}, N={N}, K={K}: got "
-                                 f"{t[name].numel() if name in t else 'none'}")
+            want |= {"idx8": (E * n, byte), "cb8": (sets * 256 * 8, half)}
+        for name, (count, types) in want.items():
+            if name not in t or t[name].numel() != count or t[name].dtype not in types:
+                got = f"{t[name].numel()} of {t[name].dtype}" if name in t else "none"
+                raise ValueError(f"{name} must have {count} entries of one of {list(types)} for E={E}, N={N}, K={K}: got {got}")
         self.bias = None
         if bias is not None:
             self.bias = bias.to(dev)
