@@ -78,6 +78,8 @@ class VQExperts:
             if name not in t or t[name].numel() != count or t[name].dtype not in types:
                 got = f"{t[name].numel()} of {t[name].dtype}" if name in t else "none"
                 raise ValueError(f"{name} must have {count} entries of one of {list(types)} for E={E}, N={N}, K={K}: got {got}")
+        if ladder and len(self.mult) != self.n16 + self.n8 - 1:
+            raise ValueError(f"mult must have {self.n16 + self.n8 - 1} entries, one per residual stage: got {len(self.mult)}")
         self.bias = None
         if bias is not None:
             self.bias = bias.to(dev)

@@ -63,3 +63,10 @@ def test_types(fmt, name):
     for b in bad:
         with pytest.raises(ValueError, match=f"{name} must"):
             make(fmt, **{name: b})
+
+
+@pytest.mark.parametrize("mult", [[], [0.5], [0.5, 0.25, 0.125]])
+def test_a_multiplier_for_every_residual_stage(mult):
+    """Two 16-bit stages and an 8-bit one have two residual stages."""
+    with pytest.raises(ValueError, match="mult must have 2"):
+        make(VQ_FMT_VQ16_RVQ, mult=mult)
