@@ -55,14 +55,12 @@ constexpr uint32_t kXtOffBars = kXtOffTiles + (sizeof(ExpertTiles) + 15) / 16 * 
 constexpr uint32_t kXtOffIdx = kXtOffBars + 768;
 constexpr uint32_t kXtOffX = (kXtOffIdx + kXtSlots * kXtIdxSlot + 1023) / 1024 * 1024;
 // Tmax is 128 or 256 (twice the heights of the larger boxes).
-// At least 144 KiB, so that no other kernel of this library that allocates TMEM (94 KiB and more a
-// block) shares the SM: a pair takes all 512 columns of both SMs, and two pairs that each hold one
-// SM's TMEM and wait for the other's would never go on.
-constexpr uint32_t xt_smem(int Tmax) {
-  const uint32_t need = kXtOffX + kXtStages * (Tmax / 2) * 256u + 1024u;
-  return need < 147456u ? 147456u : need;
-}
+constexpr uint32_t xt_smem(int Tmax) { return kXtOffX + kXtStages * (Tmax / 2) * 256u + 1024u; }
 static_assert(xt_smem(kXtMaxT) <= 232448, "shared memory of the widest tile");
+// A pair takes all 512 TMEM columns of both SMs, and two pairs that each hold one SM's and wait for
+// the other's would never go on, nor a pair and a tc_gemm_kernel block: no two of them fit an SM's
+// 228 KiB (tc_gemm_kernel takes 92 KiB and more).
+static_assert(xt_smem(kXtMaxT / 2) >= 147456, "no other block that allocates TMEM may share the SM");
 
 constexpr int kXtBoxes = 3;        // x rows of one TMA load: 32, 64 or 128
 constexpr int kXtTileCost = 600;   // cost of a tile's decode, in x rows (13.6 us + 23 ns a row at K = 2048)
@@ -169,7 +167,7 @@ __global__ void __launch_bounds__(kXtThreads, 1)
   const int out_tile = a.glu ? kXtRows / 2 : kXtRows;  // columns of y of the block's half of a tile
   const uint32_t rank = __shfl_sync(0xffffffffu, cluster_rank(), 0);
   const int RT = (a.Nout + 2 * out_tile - 1) / (2 * out_tile);  // row tiles of the pair
-  const uint32_t acols = ((uint32_t)Tmax + 31u) & ~31u;
+  const uint32_t acols = (uint32_t)Tmax;
   const uint32_t acol0 = acols * nacc;  // then the A stages
   const uint32_t tcols = 512u;  // acol0 + kXtParts * kXtACols is above 256
 
@@ -697,7 +695,7 @@ static cudaError_t launch_xt_t(ExpertsArgs a, void* xs, int Tmax, int num_sms, c
   const int smem = (int)xt_smem(Tmax);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int nacc = 2 * ((Tmax + 31) / 32 * 32) + kXtParts * (int)kXtACols <= 512 ? 2 : 1;
+  const int nacc = 2 * Tmax + kXtParts * (int)kXtACols <= 512 ? 2 : 1;
   cfg.gridDim = dim3(num_sms / 2 * 2);
   cfg.blockDim = dim3(kXtThreads);
   cfg.dynamicSmemBytes = smem;
