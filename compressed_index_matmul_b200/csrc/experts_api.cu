@@ -35,6 +35,9 @@ struct ExpertsPlan {
 // tiles) 54 / 56, x 8 (up to 18) 74 / 56, x 32 179 / 57; 8 x 1 (2048 x 2048 gated, 64 tiles) 18.0 /
 // 20.7, x 16 21.3 / 20.8; 8 x 2 (1024 x 576, 32 tiles) 8.5 / 13.0; 2 x 1 (2048 x 2048 gated, 16
 // tiles) 9.4 / 19.6; 16-bit indices, 16 x 12 (1536 x 576, 96 tiles) 19.4 / 21.8, x 25 27.5 / 22.7.
+// The formats share the thresholds; between those points nothing was measured.  The average says
+// nothing of the spread: 128 rows that all go to one of 64 experts run on the warp-MMA kernel,
+// which decodes that expert's weights eight times.
 ExpertsPlan plan_experts(const vq_experts_desc& d, int T, int forced, int num_sms) {
   const int busy = T < d.E ? T : d.E;
   const int avg = (T + busy - 1) / busy;

@@ -549,8 +549,9 @@ __global__ void __launch_bounds__(kXtThreads, 1)
         }
         if (kStaged) {
           // The slot is free once every lane's bytes are in its registers.  Which lane says so depends
-          // on the bytes, so that no load can be moved behind the arrival: with lane 0 arriving after a
-          // __syncwarp, the scales of 16-bit layers were at times those of four slices later.
+          // on the bytes, so the arrival comes after them whatever order the loads complete in: with
+          // lane 0 arriving after a __syncwarp, the scales of 16-bit layers were at times those of four
+          // slices later (why that order did not hold was not established).
           uint32_t seen = sc2;
 #pragma unroll
           for (int i = 0; i < (k16 ? 8 : 4); ++i) seen ^= lo[i];

@@ -40,7 +40,8 @@
 // global memory instead.
 // The kernel and its launcher are templates over the fused epilogue: tc_gemm.cu compiles them
 // without it, tc_gemm_fused.cu with it, so that its loads and activations take no registers from
-// a plain forward.
+// a plain forward.  With it the layouts of 96 registers spill 8 to 20 bytes a thread around the
+// epilogue, the wide tiles' (128 registers) none.
 #pragma once
 
 #include <cuda.h>
@@ -66,8 +67,8 @@ __host__ __device__ constexpr int tc_threads(int parts) { return 64 + 32 * 4 * p
 constexpr int kTcMaxT = 256;
 constexpr uint32_t kTcACols = 32;   // TMEM columns of one A stage (64 k of 16-bit pairs)
 // index-slice ring slot: lo 16 B, hi4 8 B, s2 8 B, scales 4 B per row (idx16: 32 B per row)
-constexpr uint32_t kTcIdxLo = 0, kTcIdxHi = 2048, kTcIdxS2 = kTcIdxHi + 1024, kTcIdxSc = 4096;
-constexpr uint32_t kTcIdxSlot = 4608;
+constexpr uint32_t kTcIdxLo = 0, kTcIdxHi = 16 * kTcRows, kTcIdxS2 = 24 * kTcRows, kTcIdxSc = 32 * kTcRows;
+constexpr uint32_t kTcIdxSlot = 36 * kTcRows;
 constexpr int kTcIdxSlots = 4;
 constexpr uint32_t kTcOffBars = 65536;   // after the 64 KiB codebook
 constexpr uint32_t kTcOffIdx = 65792;    // index ring
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(tc_threads(kTcParts), kTcParts == 2 ? 2 : 1)
         // Its slot held slice (kb-5)/2, which the warps decoding blocks kb - 5 and
         // kb - 4 released before decoding them; the stage-empty wait above already
         // saw MMA kb - kSt >= kb - 4 (and so every earlier block) complete, so this
-        // wait never holds back the x loads.
+        // wait never holds back the x loads.  It is also what makes the refill safe however
+        // late a load of the slot returns: the MMA came after the weights decoded from its bytes.
         if (kStaged && (kb & 1) == 1 && kb >= 5 && (kb + 3) / 2 == issued_idx && issued_idx < nsl) {
           const int j = issued_idx;
           if (!ptx::mbar_wait(idx_empty(j % kTcIdxSlots), ((j / kTcIdxSlots) - 1) & 1, p.err)) {

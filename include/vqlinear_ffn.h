@@ -20,7 +20,8 @@
 extern "C" {
 #endif
 
-/* Activations act(v), computed in fp32. */
+/* Activations act(v), computed in fp32 (SiLU and the tanh form of GELU give 0 where they are below
+ * |v| 2^-126). */
 enum {
   VQ_ACT_NONE = 0,     /* v */
   VQ_ACT_RELU = 1,     /* max(v, 0) */
@@ -99,8 +100,9 @@ vq_status vq_experts_destroy(vq_experts_t h);
  *   y        [T][N] (glu: [T][N/2]), act_dtype.  Rows below offsets[0] or from offsets[E]
  *            on are left as they were.  A y that overlaps an input is VQ_ERR_INVALID_ARG.
  * Accumulation is fp32.  The weights are rounded to act_dtype before the product, as
- * the single-layer paths that materialise weights do (the scaled stage sum with one fused
- * multiply-add per stage in fp32).  For a given kernel (below) the result of a row does not
+ * the single-layer paths that materialise weights do: the stage sum in fp32 (one addition, or one
+ * fused multiply-add per residual stage of the ladder), times the scale, rounded to fp32 and then
+ * to act_dtype.  For a given kernel (below) the result of a row does not
  * depend on the other rows, and is bit-identical from run to run.
  * Enqueues one kernel on `stream` (two where VQ_PATH_TC is given rows); nothing for T == 0. */
 vq_status vq_experts_forward(vq_experts_t h, const void* x, int32_t x_rows, const int32_t* rows,
