@@ -7,8 +7,7 @@
 //           rows of x, over all of K; the tiles of all experts are numbered in expert order
 //           (find_tiles) and cut into one contiguous, equal range per block
 //   block   16 warps with 128 registers each, one block per SM (a 17th warp, for the copies, would
-//           leave 96: 88 us for 64 experts x 4 rows of 2048 x 1024, against 70 before the loads
-//           went ahead across tiles, and 55 now).  The warps form
+//           leave 96: 88 us for 64 experts x 4 rows of 2048 x 1024, against 70; 67 now).  The warps form
 //           groups of wk; a group takes a tile at a time and its warps take the 128-input
 //           slices of K in turn.  A warp walks (tile, slice) as one sequence and
 //           loads the index bytes of its next slice before it decodes the current one, across
@@ -26,10 +25,10 @@
 // row does not depend on the other rows.
 // Bound: the shared-memory pipe.  A gather of 32 codewords of 16 bytes takes about 10 wavefronts
 // (random banks), the stage-2 codewords 4 shuffles, x and the indices the rest: 20 cycles of an SM for 256
-// weights, 3.7 T weights a second on 148 SMs at 1.965 GHz.  Measured 2.4 for 134 M weights (64 experts x 4
-// rows of 2048 x 1024, 55 us), the launch, the offsets and the codebooks included; 1.7 for 34 M (8 experts
-// x 1 row of 2048 x 2048, 19.6 us), where the shared-memory pipe is 41 % busy: the chains of
-// load, gather and MMA of 16 warps do not fill it.
+// weights, 3.7 T weights a second on 148 SMs at 1.965 GHz.  Measured, the launch, the offsets and the
+// codebooks included: 2.1 for 88 M weights (42 experts x 1 to 4 rows of 2048 x 1024, 41 us), 1.7 for
+// 34 M (8 experts x 1 row of 2048 x 2048, 19.6 us), where the shared-memory pipe is 41 % busy: the
+// chains of load, gather and MMA of 16 warps do not fill it.
 #include <type_traits>
 
 #include "experts.cuh"

@@ -16,7 +16,7 @@
 //     and of all blocks.  No atomic decides an order: the result is the same every time.
 //   - Up to 2 kRouteTile tokens one block does all of it in one launch.
 // A prompt is bound by the choices' instructions, a chain of reductions each: 8192 tokens of 128
-// experts, k = 8, take 14.9 us, nearly all of it in the first kernel, which uses half of its issue
+// experts, k = 8, take 15 us, nearly all of it in the first kernel, which uses half of its issue
 // slots and moves 4.2 MB.
 //
 // Combine.  out[t] = sum_j w[t][j] y[slot[t][j]] + residual[t]: every y row is read once
