@@ -63,3 +63,42 @@ def test_plain_forwards_for_another_stream():
             for s in (torch.cuda.default_stream(), 0):
                 assert call(s).data_ptr() == at
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tokens", [1, 40, 600])
+def test_operators_of_several_streams_at_once(tokens):
+    """Blocks of experts on two streams (handles of their own) beside dense fused forwards on a third, none waiting
+    for another: the results of the calls one after another, bit for bit."""
+    E, k, H, I = 16, 4, 512, 384
+    made = []
+    for seed in (31, 32):
+        _, up = make_experts(E, 2 * I, H, FMT_RVQ12_4, 64, seed)
+        _, down = make_experts(E, H, I, FMT_RVQ12_4, 64, seed + 10)
+        R = vq.VQRouter(E, k, tokens, renorm=True)
+        U = vq.VQExperts(E, 2 * I, H, FMT_RVQ12_4, 64, DT_BF16, tokens * k, up, act=vq.VQ_ACT_SILU, glu=True)
+        D = vq.VQExperts(E, H, I, FMT_RVQ12_4, 64, DT_BF16, tokens * k, down)
+        x, logits = randn((tokens, H), DT_BF16, seed), randn((tokens, E), DT_BF16, seed + 1)
+
+        def block(s, R=R, U=U, D=D, x=x, logits=logits):
+            r = R.forward(logits, stream=s)
+            h = U.forward(x, r.offsets, rows=r.rows, stream=s)
+            return vq.combine(D.forward(h, r.offsets, stream=s), r.weights, r.slots, residual=x, stream=s)
+
+        made.append(block)
+    _, arrays = make_experts(1, 2048, 1024, FMT_RVQ12_4, 64, 51)
+    L = vq.VQLinear(2048, 1024, FMT_RVQ12_4, 64, DT_BF16, 600, {n: v[0] for n, v in arrays.items()})
+    xs = [randn((M, 1024), DT_BF16, M) for M in (1, 9, 64, 600)]
+    made.append(lambda s: torch.cat([L.forward_fused(x, act=vq.VQ_ACT_GELU, stream=s) for x in xs]))
+    torch.cuda.synchronize()
+    want = [call(None) for call in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[] for _ in made]
+    for _ in range(25):
+        for i, call in enumerate(made):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call(streams[i] if i % 2 else None))
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        assert all(torch.equal(y.view(torch.int16), w.view(torch.int16)) for y in many)
+    vq.vq_linear_check(L.handle)
