@@ -5,7 +5,7 @@ namespace vq {
 
 bool plan_tc(const vq_linear_desc& d, const DeviceInfo& dev, int M, Plan* p) {
   if (M < 1 || dev.smem_optin < (int)kTcSmemMax) return false;
-  const TcGeom g = tc_geom(d.fmt, M, d.N, d.K, dev.num_sms);
+  const TcGeom g = tc_geom(d.fmt, d.n16, d.n8, M, d.N, d.K, dev.num_sms);
   p->path = VQ_PATH_TC;
   p->splits = g.S;
   p->k_per_split = g.kps;

@@ -607,20 +607,34 @@ struct TcGeom {
   bool dual;  // two CTAs per SM (2 decode warps per lane quarter; 3 stages for 64-token tiles)
 };
 
-// Estimated time in us of a forward cut into S splits of K, the fixed part left out: the 128-input
-// slices that a CTA decodes one after the other (0.8 us each, 1.2 with 16-bit indices; two CTAs that
-// share an SM take 1.7 times as long), and the sum over the splits: a cluster pair exchanges half
-// of its sums over distributed shared memory, more splits write theirs to global memory, from where
-// the last CTA of a tile reads them all, a split after the other.  Fitted to 20 layer shapes from
-// 1003 x 960 to 4096 x 14336 at M = 8 to 300, each forced to 1, 2, 3, 4 and 8 splits.
-static float tc_split_cost(const TcGeom& g, int S, bool k16, bool pair_ok, int nsl, int num_sms) {
+// Time in us that a CTA takes to decode a 128-input slice.  The 12-bit formats gather from shared memory: 0.7
+// to 0.9 at every T.  16-bit codewords come through L1, of which a CTA's x stages take the more the larger T
+// is, and the residual ladder gathers once more per stage.  Measured with one split, tiles of 16-48 / 64-208 /
+// 224-256 tokens: one stage 1.2 / 1.3 / 2.3; the ladder with 1 16-bit stage 2.1 / 2.6 / 3.1, 2 3.2 / 4.0 / 5.2, 3
+// 4.6 / 5.6 / 7.5, 4 5.9 / 7.3 / 9.7, and 0.6 to 1.1 more with an 8-bit one.  The 16-bit values stand 10 % above
+// that: with every SM gathering a slice takes longer, and a split too few costs more than one too many.
+static float tc_slice_cost(int fmt, int n16, int n8, int T) {
+  if (fmt != kFmtVq16 && fmt != kFmtVq16Rvq) return 0.8f;
+  const float narrow = fmt == kFmtVq16 ? 1.375f : 2.2f + 1.43f * (float)(n16 - 1) + 0.825f * (float)n8;
+  return narrow * (T < 64 ? 1.f : T <= 208 ? 1.25f : 1.7f);
+}
+
+// Estimated time in us of a forward cut into S splits of K, the fixed part left out: the slices that a
+// CTA decodes one after the other (`slice` each; two CTAs that share an SM take 1.7 times as long), and
+// the sum over the splits: a cluster pair exchanges half of its sums over distributed shared memory,
+// more splits write theirs to global memory, from where the last CTA of a tile reads them all, a split
+// after the other.  On 550 random shapes of all formats (M = 9 to 700, K = 256 to 12800), each forced to
+// every count of splits, the chosen one takes 1.01 to 1.03 times as long as the best in each format's
+// geometric mean; against as many splits as fit 0.68 (one 12-bit stage), 0.75 (12 + 4 bits), 0.84 (16
+// bits), 0.91 (the ladder's one stage) to 1.00 (its four).
+static float tc_split_cost(const TcGeom& g, int S, float slice, bool pair_ok, int nsl, int num_sms) {
   const int sps = (nsl + S - 1) / S, n = (nsl + sps - 1) / sps;
-  const float decode = (k16 ? 1.2f : 0.8f) * (float)sps * (g.RT * g.TT * n > num_sms ? 1.7f : 1.f), T = (float)g.T;
+  const float decode = slice * (float)sps * (g.RT * g.TT * n > num_sms ? 1.7f : 1.f), T = (float)g.T;
   return decode + (n == 1 ? 0.f : n == 2 && pair_ok ? 0.4f + 0.01f * T : T * (0.033f + 0.0163f * (float)n));
 }
 
-// fmt: kFmt* (the same values as VQ_FMT_*).
-static TcGeom tc_geom(int fmt, int M, int N, int K, int num_sms) {
+// fmt: kFmt* (the same values as VQ_FMT_*); n16, n8: the ladder's stages.
+static TcGeom tc_geom(int fmt, int n16, int n8, int M, int N, int K, int num_sms) {
   TcGeom g;
   const int m16 = (M + 15) / 16 * 16;
   g.T = m16 < kTcMaxT ? m16 : kTcMaxT;
@@ -646,10 +660,11 @@ static TcGeom tc_geom(int fmt, int M, int N, int K, int num_sms) {
   // The split that costs least, among those that fit the SMs.  With as many as fit, us: 2048 x 2048
   // M = 256 48.5, with the 2 chosen 14.4; M = 100 25.8, with 2 12.6; 1003 x 960 M = 77 18.8, with 1 9.7;
   // 4096 x 4096 M = 128 24.1, with 2 19.5; M = 16 16.1, with 4 14.6.  4096 x 14336 M = 16 keeps its 8
-  // (29.1; 30.9 with 4), 4096 x 4096 M = 8 on 16-bit indices its 4 (17.8; 25.0 with 2).
-  const bool k16 = fmt == kFmtVq16 || fmt == kFmtVq16Rvq;
+  // (29.1; 30.9 with 4), 4096 x 4096 M = 8 on 16-bit indices its 4 (17.8; 25.0 with 2), 288 x 8896
+  // M = 279 of a ladder of three 16-bit stages its 8 (106; 271 with 2).
+  const float slice = tc_slice_cost(fmt, n16, n8, g.T);
   for (int s = S - 1; s >= 1; --s)
-    if (tc_split_cost(g, s, k16, N % 8 == 0, nsl, num_sms) < tc_split_cost(g, S, k16, N % 8 == 0, nsl, num_sms)) S = s;
+    if (tc_split_cost(g, s, slice, N % 8 == 0, nsl, num_sms) < tc_split_cost(g, S, slice, N % 8 == 0, nsl, num_sms)) S = s;
   const int sps = (nsl + S - 1) / S;
   g.S = (nsl + sps - 1) / sps;
   g.kps = sps * 128;
@@ -750,7 +765,7 @@ static cudaError_t launch_tc_f(const LayerArgs& a, const Plan& pl, float* scratc
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const TcGeom g = tc_geom(a.fmt, a.M, a.N, a.K, sms);
+  const TcGeom g = tc_geom(a.fmt, a.n16, a.n8, a.M, a.N, a.K, sms);
   if (g.S != pl.splits) return cudaErrorInvalidValue;
   const bool bf = a.act == VQ_BF16;
   switch (a.fmt) {

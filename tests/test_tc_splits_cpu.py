@@ -20,8 +20,9 @@ CASES = [
     (2048, 8192, FMT_RVQ12, 0, DT_F16, 100, 5, 80),
     (1003, 4096, FMT_RVQ12_4, 0, DT_BF16, 100, 4, 32),    # the same with odd N
     (300, 14336, FMT_RVQ12_4, 0, DT_F16, 300, 4, 24),     # two token tiles, 44 tokens in the second, ragged rows
-    (1024, 8192, FMT_VQ16, 0, DT_BF16, 100, 6, 48),
-    (1003, 4096, FMT_VQ16_RVQ, 5, DT_F16, 70, 4, 32),
+    (1024, 8192, FMT_VQ16, 0, DT_BF16, 100, 8, 64),
+    (1003, 4096, FMT_VQ16_RVQ, 5, DT_F16, 70, 8, 64),
+    (264, 384, FMT_VQ16_RVQ, 5, DT_BF16, 100, 2, 6),      # the ladder as a pair
     (4096, 4096, FMT_RVQ12_4, 0, DT_F16, 64, 4, 128),     # 64 tokens, too many splits for two CTAs per SM
     # 64 tokens, two CTAs per SM, three x stages
     (14336, 2048, FMT_RVQ12_4, 0, DT_BF16, 64, 2, 224),   # a pair
@@ -35,7 +36,7 @@ CASES = [
     # 16-bit indices, 16 to 48 tokens, one CTA per SM
     (1024, 8192, FMT_VQ16, 0, DT_F16, 24, 8, 64),
     (264, 1024, FMT_VQ16, 0, DT_BF16, 40, 2, 6),
-    (264, 2048, FMT_VQ16_RVQ, 5, DT_BF16, 40, 4, 12),
+    (264, 2048, FMT_VQ16_RVQ, 5, DT_BF16, 40, 8, 24),
 ]
 
 
@@ -49,3 +50,22 @@ def test_splits_on_a_b200(case):
     N, K, fmt, bpw, dt, M, splits, ctas = case
     p = vq.vq_plan_for_device(N, K, fmt, 64, dt, M, M, path=vq.VQ_PATH_TC, **LADDER.get(bpw, {}))
     assert (p["path"], p["launches"], p["splits"], p["ctas"]) == (vq.VQ_PATH_TC, 1, splits, ctas)
+
+
+# (N, K, fmt, bits per weight, M, fewest splits): us with those splits or more / with 2.
+@pytest.mark.parametrize("N,K,fmt,bpw,M,fewest", [
+    (288, 8896, FMT_VQ16_RVQ, 6, 279, 7),     # 106 / 271
+    (840, 5696, FMT_VQ16_RVQ, 6, 216, 6),     # 80 / 182
+    (2592, 2432, FMT_VQ16_RVQ, 8, 79, 7),     # 38 / 78
+    (1184, 1472, FMT_VQ16_RVQ, 6, 36, 6),     # 20 / 32
+    (160, 768, FMT_VQ16_RVQ, 8, 18, 6),       # 19 / 26
+    (1144, 2816, FMT_VQ16_RVQ, 4, 600, 3),    # 65 / 68
+    (168, 8896, FMT_VQ16, 2, 545, 5),         # 59 / 86
+])
+def test_a_slower_decode_keeps_more_splits(N, K, fmt, bpw, M, fewest):
+    """A residual stage is one more gather per group: what a split saves grows with the stages, what the sum
+    over the splits costs does not."""
+    libbuild.build()
+    ladder = dict(n16=bpw // 2, n8=bpw % 2, mult=(0.5,) * (bpw // 2 + bpw % 2 - 1)) if fmt == FMT_VQ16_RVQ else {}
+    p = vq.vq_plan_for_device(N, K, fmt, 64, DT_F16, M, M, path=vq.VQ_PATH_TC, **ladder)
+    assert p["splits"] >= fewest
