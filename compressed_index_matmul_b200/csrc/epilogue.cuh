@@ -63,13 +63,15 @@ __device__ __forceinline__ float apply_act(int act, float v) {
   return f[0];
 }
 
-// Output (m, n) with at = m N + n: the sparse correction's term, then the epilogue.
+// Output (m, n) with at = m N + n: the sparse correction's term, then (kFused) the epilogue.
 // mul and residual are read with plain loads: either may be y itself (each element is
-// read and then written by one thread).
-template <typename T>
+// read and then written by one thread).  The small kernels are compiled with and without it too:
+// jumped over in one instantiation it cost a short plain forward up to 0.6 us (6640 x 192 M = 4 2.6 us,
+// 3.2 so).
+template <typename T, bool kFused>
 __device__ __forceinline__ float finish(const LayerArgs& a, int64_t at, int n, float f) {
   if (a.addend) f += a.addend[at];  // the sparse correction's x . C^T term
-  if (a.epi) {
+  if (kFused) {
     const float u = a.mul ? Elt<T>::to_f32(a.mul[at]) : 1.f;
     const float r = a.res ? Elt<T>::to_f32(a.res[at]) : 0.f;
     if (a.bias) f += Elt<T>::to_f32(a.bias[n]);

@@ -91,7 +91,7 @@ __device__ __forceinline__ void load_block(const LayerArgs& a, const int rows[2]
   b.sc = s16[0] | (s16[1] << 16);
 }
 
-template <int FMT, typename T, int NT>
+template <int FMT, typename T, int NT, bool kFused>
 __global__ void __launch_bounds__(256) gemv_kernel(LayerArgs a, int k_per_split, int splits, float* __restrict__ partial,
                                                    uint32_t* __restrict__ tickets) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(256) gemv_kernel(LayerArgs a, int k_per_split,
       for (int i = 0; i < 4; ++i) {
         const int m = 8 * t + 2 * c + (i & 1);
         const int r = rows[i >> 1];
-        if (m < M && r < N) y[(int64_t)m * N + r] = Elt<T>::from_f32(finish<T>(a, (int64_t)m * N + r, r, acc[t][i]));
+        if (m < M && r < N) y[(int64_t)m * N + r] = Elt<T>::from_f32(finish<T, kFused>(a, (int64_t)m * N + r, r, acc[t][i]));
       }
     return;
   }
@@ -234,18 +234,18 @@ __global__ void __launch_bounds__(256) gemv_kernel(LayerArgs a, int k_per_split,
     const int m = i / nrows, r = rbeg + i % nrows;
     float sum = 0.f;
     for (int k = 0; k < splits; ++k) sum += __ldcg(partial + ((int64_t)k * M + m) * N + r);
-    y[(int64_t)m * N + r] = Elt<T>::from_f32(finish<T>(a, (int64_t)m * N + r, r, sum));
+    y[(int64_t)m * N + r] = Elt<T>::from_f32(finish<T, kFused>(a, (int64_t)m * N + r, r, sum));
   }
   if (threadIdx.x == 0) tickets[blockIdx.x] = 0u;  // ready for the next forward
 }
 
-template <int FMT, typename T, int NT>
+template <int FMT, typename T, int NT, bool kFused>
 static cudaError_t launch_one(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* tickets, cudaStream_t s) {
   const int kc = p.k_per_split;
   const bool k16 = (FMT == kFmtVq16 || FMT == kFmtVq16Rvq);
   const size_t smem = (!k16 ? 4096 * 16 : 0) + (FMT == kFmtVq16Rvq ? 256 * 16 : 0) + (FMT == kFmtRvq12_4 ? 256 : 0) + 16 +
                       (size_t)8 * NT * (kc + 8) * 2;
-  auto kern = gemv_kernel<FMT, T, NT>;
+  auto kern = gemv_kernel<FMT, T, NT, kFused>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -262,24 +262,30 @@ static cudaError_t launch_one(const LayerArgs& a, const Plan& p, float* scratch,
                             p.splits > 1 ? tickets : nullptr);
 }
 
-template <int FMT, typename T>
+template <int FMT, typename T, bool kFused>
 static cudaError_t launch_nt(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* tickets, cudaStream_t s) {
-  return a.M <= 8 ? launch_one<FMT, T, 1>(a, p, scratch, tickets, s) : launch_one<FMT, T, 2>(a, p, scratch, tickets, s);
+  return a.M <= 8 ? launch_one<FMT, T, 1, kFused>(a, p, scratch, tickets, s)
+                  : launch_one<FMT, T, 2, kFused>(a, p, scratch, tickets, s);
 }
 
-template <typename T>
+template <typename T, bool kFused>
 static cudaError_t launch_fmt(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* tickets, cudaStream_t s) {
   switch (a.fmt) {
-    case kFmtRvq12: return launch_nt<kFmtRvq12, T>(a, p, scratch, tickets, s);
-    case kFmtRvq12_4: return launch_nt<kFmtRvq12_4, T>(a, p, scratch, tickets, s);
-    case kFmtVq16Rvq: return launch_nt<kFmtVq16Rvq, T>(a, p, scratch, tickets, s);
-    default: return launch_nt<kFmtVq16, T>(a, p, scratch, tickets, s);
+    case kFmtRvq12: return launch_nt<kFmtRvq12, T, kFused>(a, p, scratch, tickets, s);
+    case kFmtRvq12_4: return launch_nt<kFmtRvq12_4, T, kFused>(a, p, scratch, tickets, s);
+    case kFmtVq16Rvq: return launch_nt<kFmtVq16Rvq, T, kFused>(a, p, scratch, tickets, s);
+    default: return launch_nt<kFmtVq16, T, kFused>(a, p, scratch, tickets, s);
   }
 }
 
+template <bool kFused>
+static cudaError_t launch_act(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* tickets, cudaStream_t s) {
+  return a.act == VQ_BF16 ? launch_fmt<__nv_bfloat16, kFused>(a, p, scratch, tickets, s)
+                          : launch_fmt<__half, kFused>(a, p, scratch, tickets, s);
+}
+
 cudaError_t launch_gemv(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* tickets, cudaStream_t s) {
-  return a.act == VQ_BF16 ? launch_fmt<__nv_bfloat16>(a, p, scratch, tickets, s)
-                          : launch_fmt<__half>(a, p, scratch, tickets, s);
+  return a.epi ? launch_act<true>(a, p, scratch, tickets, s) : launch_act<false>(a, p, scratch, tickets, s);
 }
 
 // Split choice: enough CTAs to cover the SMs about twice, each K-split a multiple

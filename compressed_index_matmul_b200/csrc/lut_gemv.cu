@@ -153,7 +153,7 @@ __device__ __forceinline__ void lookup_row(const uint4& lo4, const uint2& h, con
   }
 }
 
-template <int FMT, typename T>
+template <int FMT, typename T, bool kFused>
 __global__ void __launch_bounds__(kLutThreads, 1)
     lut_gemv_kernel(LayerArgs a, float* __restrict__ partial, uint32_t* __restrict__ sync, uint32_t* __restrict__ err,
                     int S) {
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kLutThreads, 1)
         }
         if (S == 1) {
           if (!block_scales) acc *= f16_bits_to_f32(a.scales[r]);
-          static_cast<uint16_t*>(a.y)[r] = Elt<T>::from_f32(finish<T>(a, r, r, acc));
+          static_cast<uint16_t*>(a.y)[r] = Elt<T>::from_f32(finish<T, kFused>(a, r, r, acc));
         } else {
           partial[(int64_t)s * N + r] = acc;
         }
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kLutThreads, 1)
         for (int i = 0; i < 4; ++i) o4[i] *= f16_bits_to_f32(a.scales[r + i]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o4[i] = finish<T>(a, r + i, r + i, o4[i]);
+      for (int i = 0; i < 4; ++i) o4[i] = finish<T, kFused>(a, r + i, r + i, o4[i]);
       uint16_t* yr = static_cast<uint16_t*>(a.y) + r;
       *reinterpret_cast<uint2*>(yr) =
           make_uint2((uint32_t)Elt<T>::from_f32(o4[0]) | ((uint32_t)Elt<T>::from_f32(o4[1]) << 16),
@@ -519,11 +519,11 @@ bool plan_lut(const vq_linear_desc& d, const DeviceInfo& dev, int M, Plan* p) {
   return true;
 }
 
-template <int FMT, typename T>
+template <int FMT, typename T, bool kFused>
 static cudaError_t launch_lut_t(const LayerArgs& a, int grid, float* scratch, uint32_t* sync, uint32_t* err,
                                 cudaStream_t s) {
   const int S = a.K / (8 * kLutGroups);
-  auto kern = lut_gemv_kernel<FMT, T>;
+  auto kern = lut_gemv_kernel<FMT, T, kFused>;
   // The shared-memory opt-in is a per-device property of the function: set it
   // once per device (repeating it from two threads is harmless).
   static std::atomic<uint64_t> opted{0};
@@ -554,13 +554,19 @@ static cudaError_t launch_lut_t(const LayerArgs& a, int grid, float* scratch, ui
   return cudaLaunchKernelEx(&cfg, kern, a, S > 1 ? scratch : nullptr, sync, err, S);
 }
 
+template <bool kFused>
+static cudaError_t launch_lut_f(const LayerArgs& a, int grid, float* scratch, uint32_t* sync, uint32_t* err,
+                                cudaStream_t s) {
+  if (a.fmt == kFmtRvq12_4)
+    return a.act == VQ_BF16 ? launch_lut_t<kFmtRvq12_4, __nv_bfloat16, kFused>(a, grid, scratch, sync, err, s)
+                            : launch_lut_t<kFmtRvq12_4, __half, kFused>(a, grid, scratch, sync, err, s);
+  return a.act == VQ_BF16 ? launch_lut_t<kFmtRvq12, __nv_bfloat16, kFused>(a, grid, scratch, sync, err, s)
+                          : launch_lut_t<kFmtRvq12, __half, kFused>(a, grid, scratch, sync, err, s);
+}
+
 cudaError_t launch_lut(const LayerArgs& a, const Plan& p, float* scratch, uint32_t* sync, uint32_t* err,
                        cudaStream_t s) {
-  if (a.fmt == kFmtRvq12_4)
-    return a.act == VQ_BF16 ? launch_lut_t<kFmtRvq12_4, __nv_bfloat16>(a, p.grid, scratch, sync, err, s)
-                            : launch_lut_t<kFmtRvq12_4, __half>(a, p.grid, scratch, sync, err, s);
-  return a.act == VQ_BF16 ? launch_lut_t<kFmtRvq12, __nv_bfloat16>(a, p.grid, scratch, sync, err, s)
-                          : launch_lut_t<kFmtRvq12, __half>(a, p.grid, scratch, sync, err, s);
+  return a.epi ? launch_lut_f<true>(a, p.grid, scratch, sync, err, s) : launch_lut_f<false>(a, p.grid, scratch, sync, err, s);
 }
 
 }  // namespace vq

@@ -118,7 +118,7 @@ struct V16Pos {
 // each residual stage t of the position is gathered the same way (its 16 indices
 // loaded then, from plane t or the 8-bit plane) and its dot products are added as
 // mult_t * (x . c_t) before the block scales.
-template <typename T, int MT, bool kLadder>
+template <typename T, int MT, bool kLadder, bool kFused>
 __global__ void __launch_bounds__(kV16Consumers, 1)
     vq16_gemv_kernel(LayerArgs a, const int8_t* __restrict__ signs, float xscale, int S, int blocks_per_cluster,
                      int rblk) {
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kV16Consumers, 1)
 #pragma unroll
         for (int q = 0; q < kV16Cluster; ++q) v += ld_cluster_f32(ptx::map_shared_rank(local, q));
         const int64_t at = (int64_t)m * N + r0 + r;
-        static_cast<uint16_t*>(a.y)[at] = Elt<T>::from_f32(finish<T>(a, at, r0 + r, v * xscale * row_scale[o]));
+        static_cast<uint16_t*>(a.y)[at] = Elt<T>::from_f32(finish<T, kFused>(a, at, r0 + r, v * xscale * row_scale[o]));
       }
     }
     ptx::cluster_sync();  // no CTA reuses or releases its csum while another reads it
@@ -352,9 +352,9 @@ static int v16_max_clusters(int num_sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(vq16_gemv_kernel<__half, 8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+  if (cudaFuncSetAttribute(vq16_gemv_kernel<__half, 8, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
           cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, vq16_gemv_kernel<__half, 8, false>, &cfg) != cudaSuccess || n < 1) {
+      cudaOccupancyMaxActiveClusters(&n, vq16_gemv_kernel<__half, 8, false, false>, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
     n = num_sms / kV16Cluster;
   }
@@ -378,10 +378,10 @@ bool plan_vq16(const vq_linear_desc& d, const DeviceInfo& dev, int M, Plan* p) {
   return true;
 }
 
-template <typename T, int MT, bool kLadder>
+template <typename T, int MT, bool kLadder, bool kFused>
 static cudaError_t launch_vq16_t(const LayerArgs& a, int grid, const int8_t* signs, cudaStream_t s) {
   const int S = a.K / 128;
-  auto kern = vq16_gemv_kernel<T, MT, kLadder>;
+  auto kern = vq16_gemv_kernel<T, MT, kLadder, kFused>;
   static std::atomic<uint64_t> opted{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -422,22 +422,27 @@ static cudaError_t launch_vq16_t(const LayerArgs& a, int grid, const int8_t* sig
   return cudaLaunchKernelEx(&cfg, kern, a, signs, xscale, S, g.blocks_per_cluster, g.rblk);
 }
 
-template <typename T, bool kLadder>
+template <typename T, bool kLadder, bool kFused>
 static cudaError_t launch_vq16_m(const LayerArgs& a, int grid, const int8_t* signs, cudaStream_t s) {
   switch (v16_mt(a.M)) {
-    case 1: return launch_vq16_t<T, 1, kLadder>(a, grid, signs, s);
-    case 2: return launch_vq16_t<T, 2, kLadder>(a, grid, signs, s);
-    case 4: return launch_vq16_t<T, 4, kLadder>(a, grid, signs, s);
-    default: return launch_vq16_t<T, 8, kLadder>(a, grid, signs, s);
+    case 1: return launch_vq16_t<T, 1, kLadder, kFused>(a, grid, signs, s);
+    case 2: return launch_vq16_t<T, 2, kLadder, kFused>(a, grid, signs, s);
+    case 4: return launch_vq16_t<T, 4, kLadder, kFused>(a, grid, signs, s);
+    default: return launch_vq16_t<T, 8, kLadder, kFused>(a, grid, signs, s);
   }
 }
 
-cudaError_t launch_vq16(const LayerArgs& a, const Plan& p, const int8_t* signs, cudaStream_t s) {
+template <bool kFused>
+static cudaError_t launch_vq16_f(const LayerArgs& a, int grid, const int8_t* signs, cudaStream_t s) {
   const bool lad = a.fmt == kFmtVq16Rvq;
   if (a.act == VQ_BF16)
-    return lad ? launch_vq16_m<__nv_bfloat16, true>(a, p.grid, signs, s)
-               : launch_vq16_m<__nv_bfloat16, false>(a, p.grid, signs, s);
-  return lad ? launch_vq16_m<__half, true>(a, p.grid, signs, s) : launch_vq16_m<__half, false>(a, p.grid, signs, s);
+    return lad ? launch_vq16_m<__nv_bfloat16, true, kFused>(a, grid, signs, s)
+               : launch_vq16_m<__nv_bfloat16, false, kFused>(a, grid, signs, s);
+  return lad ? launch_vq16_m<__half, true, kFused>(a, grid, signs, s) : launch_vq16_m<__half, false, kFused>(a, grid, signs, s);
+}
+
+cudaError_t launch_vq16(const LayerArgs& a, const Plan& p, const int8_t* signs, cudaStream_t s) {
+  return a.epi ? launch_vq16_f<true>(a, p.grid, signs, s) : launch_vq16_f<false>(a, p.grid, signs, s);
 }
 
 }  // namespace vq
