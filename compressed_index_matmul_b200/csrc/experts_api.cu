@@ -35,9 +35,12 @@ struct ExpertsPlan {
 // tiles) 54 / 56, x 8 (up to 18) 74 / 56, x 32 179 / 57; 8 x 1 (2048 x 2048 gated, 64 tiles) 18.0 /
 // 20.7, x 16 21.3 / 20.8; 8 x 2 (1024 x 576, 32 tiles) 8.5 / 13.0; 2 x 1 (2048 x 2048 gated, 16
 // tiles) 9.4 / 19.6; 16-bit indices, 16 x 12 (1536 x 576, 96 tiles) 19.4 / 21.8, x 25 27.5 / 22.7.
-// The formats share the thresholds; between those points nothing was measured.  The average says
-// nothing of the spread: 128 rows that all go to one of 64 experts run on the warp-MMA kernel,
-// which decodes that expert's weights eight times.
+// The formats share the thresholds, and the shape counts only through the SMs.  Over 6300 random calls (2 to
+// 128 experts of up to 4096 x 4096, 1 to 100 rows on average) the choice takes 1.09 times as long as the
+// faster kernel on 12-bit formats, 1.22 on 16-bit ones and 1.14 on the ladder (geometric means); at
+// worst 2.9, 4.8 and 6.6 times, where fewer than 74 tiles (3 experts of 128 x 4096) leave most pairs of the
+// tensor-core kernel without one.  The average says nothing of the spread: 128 rows that all go to
+// one of 64 experts run on the warp-MMA kernel, which decodes that expert's weights eight times.
 ExpertsPlan plan_experts(const vq_experts_desc& d, int T, int forced, int num_sms) {
   const int busy = T < d.E ? T : d.E;
   const int avg = (T + busy - 1) / busy;
